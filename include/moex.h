@@ -60,6 +60,13 @@ typedef enum moex_fmt {
   MOEX_IQ4_NL = 2  /* 32 4-bit indices into kvalues_iq4nl + FP16 scale     */
 } moex_fmt;
 
+/* Element types of activations and of a paged cache. */
+typedef enum moex_type {
+  MOEX_F32 = 0,
+  MOEX_BF16 = 1,
+  MOEX_F16 = 2
+} moex_type;
+
 /*
  * A stack of n_mats weight matrices (experts) of rows x K in packed planes
  * (#1424 What changed: GGUF blocks repacked so every load is 16 bytes):
@@ -350,9 +357,169 @@ moex_status moex_moe_decode_noalloc(const moex_qweight* gate_up, const moex_qwei
                                     const int32_t* ids, const float* w, int k, float* out, moex_stream stream);
 
 /*
+ * Residual addition and root-mean-square norm, the step before a layer's
+ * products (no counterpart on the pages; the operators from here on are the
+ * library's own, what a served layer needs around its quantized products):
+ *   s = x + residual (FP32; s = x without a residual)
+ *   y = s * gamma / sqrt(mean(s^2) + eps)
+ * and any of three outputs of it: s itself, y as rows, y as q8_1 blocks (the
+ * arithmetic of moex_quantize_q8_1 on the FP32 y, one launch instead of two).
+ *   x        : device [T][H] of x_type (F32, BF16, F16), row t at x + t*ldx.
+ *   residual : device FP32, row t at residual + t*ldr, or NULL.
+ *   gamma    : device FP32 [H].   eps > 0.
+ *   sum      : device FP32, row t at sum + t*lds, or NULL; may be residual
+ *              itself (with lds == ldr), and x itself when x is FP32.
+ *   y        : device rows of y_type (F32, BF16, F16), row t at y + t*ldy, or NULL.
+ *   q, ds    : device int8 [T][H] and float [T][H/32][2], or both NULL.
+ * H % 32 == 0, H <= 32768; row strides are multiples of 4 elements, every
+ * pointer 16-byte aligned (16-bit rows 8-byte aligned, ds 8-byte aligned).
+ * At least one output.  One launch.  A row of zeros gives zeros.
+ */
+moex_status moex_add_rms_norm(const void* x, int x_type, int64_t ldx, const float* residual, int64_t ldr,
+                              const float* gamma, float eps, int T, int64_t H, float* sum, int64_t lds, void* y,
+                              int y_type, int64_t ldy, int8_t* q, float* ds, moex_stream stream);
+
+/*
+ * The values that q8_1 rows stand for, y = d * q (one FP32 product, rounded
+ * once to y_type):
+ *   q  : device int8 [T][K] (16-byte aligned);  ds : device float [T][K/32][2];
+ *   y  : device [T][K] of y_type (F32, BF16, F16), 16-byte aligned.
+ */
+moex_status moex_dequantize_q8_1(const int8_t* q, const float* ds, int T, int64_t K, void* y, int y_type,
+                                 moex_stream stream);
+
+/* How router logits become scores. */
+typedef enum moex_score {
+  MOEX_SCORE_SOFTMAX = 0, /* softmax over all E logits of the token */
+  MOEX_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-logit)) of each logit     */
+} moex_score;
+
+/*
+ * Routing to experts in its general form (moex_route_topk is the plain one:
+ * top-k of the logits, softmax over the selected):
+ *   score[e] = softmax or sigmoid of the logits (FP32)
+ *   rank[e]  = score[e] + bias[e]         (bias only moves the selection)
+ *   a group of E/groups consecutive experts ranks by the sum of its
+ *   group_top best rank[e]; the top_groups best groups stay
+ *   ids      = the k experts of those groups with the largest rank, in
+ *              descending order; ties, of groups too, go to the lower index
+ *   w        = score[ids] (without the bias), divided by their sum when renorm
+ *              is set, times scale.
+ * An expert whose logit is -inf or NaN is masked: its score is 0 and it comes
+ * after every other expert of the groups that stay, whatever its bias, in
+ * index order; in its group's rank it counts nothing, and a group of masked
+ * experts comes after every other group.  A logit of +inf has the limit's
+ * score.  Selected scores that are all 0 give weights of 0.
+ *   logits : device [T][E] of type F32, BF16 or F16, row t at logits + t*ldl.
+ *   bias   : device FP32 [E] or NULL.
+ *   ids    : device int32 [T][k];  w : device FP32 [T][k].
+ * 1 <= k <= 16, E <= 1024, groups <= 32 divides E, group_top is 1 or 2,
+ * k <= top_groups * (E / groups).  One launch.
+ */
+moex_status moex_route_experts(const void* logits, int type, int64_t ldl, const float* bias, int T, int E, int k,
+                               int score, int groups, int top_groups, int group_top, int renorm, float scale,
+                               int32_t* ids, float* w, moex_stream stream);
+
+/*
+ * Keys and values of one layer in pages of page_size tokens.  Element d of
+ * key head h of the token in slot r of page p is at
+ *   k + p*page_stride + h*head_stride + r*row_stride + d        (elements)
+ * and its value at the same offset of v, so both [page][head][slot][dim] and
+ * [page][slot][head][dim] are taken, also as part of a larger buffer.
+ * Strides are multiples of 8 elements, k and v 16-byte aligned; page_size is a
+ * power of two from 8 to 1024.  Offsets are 64-bit.
+ */
+typedef struct moex_paged_kv {
+  int32_t type;      /* MOEX_BF16 or MOEX_F16 */
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t n_pages;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t row_stride;
+  void* k;
+  void* v;
+} moex_paged_kv;
+
+/*
+ * The new tokens of n_seqs sequences, packed one sequence after the other:
+ * sequence b has tokens cu_q[b] .. cu_q[b+1]-1 (cu_q[0] = 0, cu_q[n_seqs] =
+ * n_tokens, none is fine) and ctx_len[b] tokens in the cache, the new ones
+ * last: token i of its n has position ctx_len[b] - n + i.  Position p lives in
+ * slot p % page_size of page page_table[b*table_stride + p / page_size].
+ * max_q is the largest number of new tokens of a sequence (it picks the
+ * kernel; a wrong value costs time, not results).  What the arrays say is
+ * checked on the device: a page id outside [0, n_pages), a length beyond
+ * table_width pages or tokens beyond n_tokens are left out and flagged
+ * (MOEX_EDEVICE).
+ */
+typedef struct moex_batch {
+  int32_t n_seqs;
+  int32_t n_tokens;
+  int32_t max_q;
+  int32_t table_width;  /* pages a row of page_table holds */
+  int64_t table_stride; /* int32 elements between its rows; 0: one row for all */
+  const int32_t* cu_q;       /* device [n_seqs + 1] */
+  const int32_t* ctx_len;    /* device [n_seqs]     */
+  const int32_t* page_table; /* device              */
+} moex_batch;
+
+/*
+ * New tokens into the cache: rotary embedding of queries and keys, then keys
+ * and values to their slots and queries to q, rounded once to the cache type.
+ *   qkv     : device rows of `type` (F32, BF16, F16), token t at qkv + t*ld:
+ *             n_heads query heads, n_kv_heads key heads, n_kv_heads value heads.
+ *   cos_sin : device FP32 [n_pos][rot_dim]: row p holds rot_dim/2 cosines, then
+ *             as many sines, of position p's angles; NULL with rot_dim == 0
+ *             (no rotation).
+ *   Features i and i + rot_dim/2 of a head (interleaved == 0), or 2i and 2i+1
+ *   (interleaved == 1), turn by angle i:
+ *     (a, b) -> (a cos - b sin, b cos + a sin);
+ *   features from rot_dim on pass unchanged.
+ *   q       : device [n_tokens][n_heads][head_dim] of the cache type, token t at q + t*ldq.
+ * head_dim and rot_dim are multiples of 16, head_dim <= 512, rot_dim <=
+ * head_dim.  A token with a negative position gives a q row of zeros and
+ * writes nothing; a position of n_pos or more does the same and is flagged.
+ * One launch.
+ */
+moex_status moex_rope_kv_write(const void* qkv, int type, int64_t ld, const moex_paged_kv* kv, const moex_batch* batch,
+                               int n_heads, const float* cos_sin, int64_t n_pos, int rot_dim, int interleaved, void* q,
+                               int64_t ldq, moex_stream stream);
+
+/* Workspace bytes of moex_paged_attention (no device is asked about lengths,
+ * so it depends on the batch's shape alone). */
+size_t moex_paged_attention_workspace_bytes(const moex_paged_kv* kv, const moex_batch* batch, int n_heads);
+
+/*
+ * Causal attention of every sequence's new tokens over its paged cache (which
+ * holds the new tokens' keys and values already): token at position p, query
+ * head h, key head h / (n_heads / n_kv_heads):
+ *   out = sum_j softmax_j(scale * q.k_j) v_j   over j <= p, and j > p - window
+ *                                              when window > 0
+ *   lse = log sum_j exp(scale * q.k_j).
+ * Scores, their maximum and sum, and the accumulated output are FP32;
+ * probabilities are rounded to the cache type for the second product.  A token
+ * that sees no key gives zeros and lse = -inf.
+ *   q    : device [n_tokens][n_heads][head_dim] of the cache type, token t at q + t*ldq.
+ *   out  : device [n_tokens][n_heads][head_dim] of out_type (the cache type or
+ *          F32), token t at out + t*ldo.
+ *   lse  : device FP32 [n_tokens][n_heads] or NULL.
+ *   ws   : device workspace of moex_paged_attention_workspace_bytes() bytes, or
+ *          NULL when that is 0.
+ * head_dim 64 or 128; n_heads a multiple of n_kv_heads, at most 128 a key
+ * head; scale > 0; ldq and ldo multiples of 8.  Results do not depend on the
+ * order in which blocks run.
+ */
+moex_status moex_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
+                                 int n_heads, float scale, int window, void* out, int out_type, int64_t ldo, float* lse,
+                                 void* ws, size_t ws_bytes, moex_stream stream);
+
+/*
  * Reads and clears the device status word after synchronising `stream`.
  * *flags receives its bits (1: routing id out of range, 2: copy-pipeline
- * wait ran out, 4: tensor-core wait ran out, 8: bad shape on the device).
+ * wait ran out, 4: tensor-core wait ran out, 8: bad shape on the device, 16: a
+ * batch's lengths, pages or positions out of range).
  * Returns MOEX_OK when the word was 0, MOEX_EDEVICE / MOEX_ETIMEOUT
  * otherwise, MOEX_ECUDA if the stream reported an error.
  */

@@ -37,11 +37,29 @@ class QWeight(ctypes.Structure):
                 ("K", ctypes.c_int64), ("qs", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class PagedKV(ctypes.Structure):
+    """moex_paged_kv: keys and values of one layer in pages."""
+    _fields_ = [("type", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p)]
+
+
+class Batch(ctypes.Structure):
+    """moex_batch: the new tokens of several sequences."""
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("table_stride", ctypes.c_int64), ("cu_q", ctypes.c_void_p),
+                ("ctx_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 _QWP = ctypes.POINTER(QWeight)
+_KVP = ctypes.POINTER(PagedKV)
+_BP = ctypes.POINTER(Batch)
 
 # name -> (restype, argtypes); mirrors include/moex.h
 SIGNATURES = {
@@ -77,6 +95,15 @@ SIGNATURES = {
                                                 _P]),
     "moex_moe_prefill_residual": (ctypes.c_int, [_QWP, _QWP, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _SZ,
                                                  _P]),
+    "moex_add_rms_norm": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, _F32, ctypes.c_int, _I64, _P, _I64, _P,
+                                         ctypes.c_int, _I64, _P, _P, _P]),
+    "moex_dequantize_q8_1": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _P, ctypes.c_int, _P]),
+    "moex_route_experts": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P] + [ctypes.c_int] * 8 + [_F32, _P, _P, _P]),
+    "moex_rope_kv_write": (ctypes.c_int, [_P, ctypes.c_int, _I64, _KVP, _BP, ctypes.c_int, _P, _I64, ctypes.c_int,
+                                          ctypes.c_int, _P, _I64, _P]),
+    "moex_paged_attention_workspace_bytes": (_SZ, [_KVP, _BP, ctypes.c_int]),
+    "moex_paged_attention": (ctypes.c_int, [_P, _I64, _KVP, _BP, ctypes.c_int, _F32, ctypes.c_int, _P, ctypes.c_int,
+                                            _I64, _P, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -391,6 +418,221 @@ def moe_decode_noalloc(gate_up: PackedWeight, down: PackedWeight, x, ids, w, out
     _check(lib().moex_moe_decode_noalloc(ctypes.byref(gate_up.struct), ctypes.byref(down.struct), _ptr(x), T,
                                          _ptr(ids), _ptr(w), k, _ptr(out), _stream(stream)),
            "moex_moe_decode_noalloc")
+    return out
+
+
+_type_codes = None
+
+
+def _type(dtype) -> int:
+    """moex_type of a torch dtype."""
+    global _type_codes
+    if _type_codes is None:
+        torch = _torch()
+        _type_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _type_codes.get(dtype)
+    if code is None:
+        raise TypeError(f"expected float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("every tensor has to be a CUDA tensor")
+
+
+def add_rms_norm(x, gamma, eps: float = 1e-6, residual=None, sum_out=None, y=None, y_dtype=None, quantize=False,
+                 q=None, ds=None, stream=None):
+    """s = x + residual, y = s * gamma / sqrt(mean(s^2) + eps), in one launch.
+
+    x [T, H] (float32, bfloat16 or float16), gamma [H] and residual [T, H]
+    float32.  Returns (s, y, q, ds): s float32 when there is a residual (or
+    sum_out is given; it may be residual itself), y when y or y_dtype is
+    given, q int8 [T, H] and ds float32 [T, H/32, 2] with quantize=True (the
+    q8_1 rows that qgemv takes); None for what was not asked for."""
+    torch = _torch()
+    T, H = x.shape
+    _need(x.stride(1) == 1 and gamma.dtype == torch.float32 and gamma.numel() == H and gamma.is_contiguous(),
+          "x rows contiguous, gamma float32 [H]")
+    if residual is not None:
+        _need(residual.shape == x.shape and residual.dtype == torch.float32 and residual.stride(1) == 1,
+              "residual: float32 [T, H]")
+        if sum_out is None:
+            sum_out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+    if sum_out is not None:
+        _need(sum_out.shape == x.shape and sum_out.dtype == torch.float32 and sum_out.stride(1) == 1,
+              "sum_out: float32 [T, H]")
+    if y is None and y_dtype is not None:
+        y = torch.empty((T, H), dtype=y_dtype, device=x.device)
+    if y is not None:
+        _need(y.shape == x.shape and y.stride(1) == 1, "y: [T, H]")
+    if quantize:
+        if q is None:
+            q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+        if ds is None:
+            ds = torch.empty((T, H // QK, 2), dtype=torch.float32, device=x.device)
+        _need(q.numel() == T * H and q.dtype == torch.int8 and q.is_contiguous() and ds.numel() == T * H // QK * 2
+              and ds.dtype == torch.float32 and ds.is_contiguous(), "q: int8 [T, H], ds: float32 [T, H/32, 2]")
+    else:
+        q = ds = None
+    _on_gpu(x, gamma, residual, sum_out, y, q, ds)
+    _check(lib().moex_add_rms_norm(
+        x.data_ptr(), _type(x.dtype), x.stride(0) if T > 1 else H,
+        None if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0) if T > 1 else H,
+        gamma.data_ptr(), eps, T, H,
+        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0) if T > 1 else H,
+        None if y is None else y.data_ptr(), 0 if y is None else _type(y.dtype),
+        0 if y is None else y.stride(0) if T > 1 else H,
+        None if q is None else q.data_ptr(), None if q is None else ds.data_ptr(), _stream(stream)),
+        "moex_add_rms_norm")
+    return sum_out, y, q, ds
+
+
+def dequantize_q8_1(q, ds, y=None, dtype=None, stream=None):
+    """The values d * q of q8_1 rows (q int8 [T, K], ds [T, K/32, 2]) as
+    float32 (default), bfloat16 or float16 rows."""
+    torch = _torch()
+    T, K = q.shape
+    if y is None:
+        y = torch.empty((T, K), dtype=dtype or torch.float32, device=q.device)
+    _need(q.is_contiguous() and ds.is_contiguous() and y.is_contiguous() and y.shape == q.shape
+          and ds.numel() == T * K // QK * 2, "q, ds, y: contiguous [T, K], [T, K/32, 2], [T, K]")
+    _on_gpu(q, ds, y)
+    _check(lib().moex_dequantize_q8_1(q.data_ptr(), ds.data_ptr(), T, K, y.data_ptr(), _type(y.dtype),
+                                      _stream(stream)), "moex_dequantize_q8_1")
+    return y
+
+
+SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                  group_top: int = 1, renorm: bool = True, scale: float = 1.0, ids=None, w=None, stream=None):
+    """Routing in its general form: softmax or sigmoid scores of the logits
+    [T, E], selection by score + bias inside the top_groups best of `groups`
+    groups (each ranked by the sum of its group_top best experts), weights =
+    the selected scores, renormalised and scaled.  Returns ids int32 [T, k]
+    and w float32 [T, k], as moe_decode and moe_prefill take them."""
+    torch = _torch()
+    T, E = logits.shape
+    _need(score in SCORE, "score: softmax or sigmoid")
+    _need(logits.stride(1) == 1, "logits rows contiguous")
+    _need(bias is None or (bias.numel() == E and bias.dtype == torch.float32 and bias.is_contiguous()),
+          "bias: float32 [E]")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous()
+          and w.shape == (T, k) and w.dtype == torch.float32 and w.is_contiguous(), "ids: int32 [T, k], w: float32 [T, k]")
+    _on_gpu(logits, bias, ids, w)
+    _check(lib().moex_route_experts(logits.data_ptr(), _type(logits.dtype), logits.stride(0) if T > 1 else E,
+                                    None if bias is None else bias.data_ptr(), T, E, k, SCORE[score], groups,
+                                    top_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(),
+                                    _stream(stream)), "moex_route_experts")
+    return ids, w
+
+
+def _paged_kv(k_cache, v_cache) -> PagedKV:
+    n_pages, heads, page, dim = k_cache.shape
+    st = k_cache.stride()
+    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype and v_cache.stride() == st and st[3] == 1,
+          "k_cache and v_cache: the same type, shape [pages, heads, page, dim] and strides, dim contiguous")
+    return PagedKV(_type(k_cache.dtype), page, heads, dim, n_pages, st[0], st[1], st[2], k_cache.data_ptr(),
+                   v_cache.data_ptr())
+
+
+def _batch(cu_q, ctx_len, page_table, n_tokens, max_q) -> Batch:
+    i32 = _torch().int32
+    n = ctx_len.numel()
+    _need(cu_q.dtype == i32 and ctx_len.dtype == i32 and page_table.dtype == i32 and cu_q.numel() == n + 1
+          and page_table.dim() == 2 and page_table.shape[0] == n and page_table.stride(1) == 1
+          and cu_q.is_contiguous() and ctx_len.is_contiguous(),
+          "cu_q: int32 [B + 1], ctx_len: int32 [B], page_table: int32 [B, width]")
+    width = page_table.shape[1]
+    return Batch(n, n_tokens, n_tokens if max_q is None else max_q, width, page_table.stride(0) if n > 1 else width,
+                 cu_q.data_ptr(), ctx_len.data_ptr(), page_table.data_ptr())
+
+
+def rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, n_heads: int, cos_sin=None,
+                  interleaved: bool = False, q=None, stream=None):
+    """New tokens into a paged cache.  qkv [T, (n_heads + 2 * kv_heads) * dim]
+    (float32, bfloat16 or float16): rotary embedding of queries and keys by
+    the table cos_sin (float32 [positions, rot_dim]: cosines, then sines; None
+    for no rotation), keys and values to their slots of k_cache / v_cache
+    [pages, kv_heads, page, dim] (any strides with dim contiguous), queries
+    returned as q [T, n_heads, dim] of the cache type.
+
+    Sequence b has new tokens cu_q[b] .. cu_q[b+1]-1 and ctx_len[b] tokens in
+    the cache, the new ones last; page_table [B, width] (all int32)."""
+    torch = _torch()
+    T = qkv.shape[0]
+    kv = _paged_kv(k_cache, v_cache)
+    b = _batch(cu_q, ctx_len, page_table, T, None)
+    _need(qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] == (n_heads + 2 * kv.n_kv_heads) * kv.head_dim,
+          "qkv: [T, (n_heads + 2 * kv_heads) * dim]")
+    rot = 0
+    if cos_sin is not None:
+        _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous(),
+              "cos_sin: float32 [positions, rot_dim]")
+        rot = cos_sin.shape[1]
+    if q is None:
+        q = torch.empty((T, n_heads, kv.head_dim), dtype=k_cache.dtype, device=qkv.device)
+    _need(q.shape == (T, n_heads, kv.head_dim) and q.dtype == k_cache.dtype and q.stride(2) == 1
+          and q.stride(1) == kv.head_dim, "q: [T, n_heads, dim] of the cache type, heads contiguous")
+    _on_gpu(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, cos_sin, q)
+    _check(lib().moex_rope_kv_write(qkv.data_ptr(), _type(qkv.dtype), qkv.stride(0) if T > 1 else qkv.shape[1],
+                                    ctypes.byref(kv), ctypes.byref(b), n_heads,
+                                    cos_sin.data_ptr() if rot else None, cos_sin.shape[0] if rot else 0, rot,
+                                    1 if interleaved else 0, q.data_ptr(),
+                                    q.stride(0) if T > 1 else n_heads * kv.head_dim, _stream(stream)),
+           "moex_rope_kv_write")
+    return q
+
+
+def paged_attention_workspace_bytes(k_cache, v_cache, cu_q, ctx_len, page_table, n_tokens: int, n_heads: int,
+                                    max_q: Optional[int] = None) -> int:
+    kv = _paged_kv(k_cache, v_cache)
+    b = _batch(cu_q, ctx_len, page_table, n_tokens, max_q)
+    return int(lib().moex_paged_attention_workspace_bytes(ctypes.byref(kv), ctypes.byref(b), n_heads))
+
+
+def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optional[int] = None,
+                    scale: Optional[float] = None, window: int = 0, out=None, out_dtype=None, lse=None, ws=None,
+                    stream=None):
+    """Causal attention of the sequences' new tokens q [T, n_heads, dim] over
+    their paged cache (see rope_kv_write for the batch; the cache holds the new
+    tokens already).  max_q: the largest number of new tokens of a sequence
+    (None: T); it picks the kernel.  scale: 1/sqrt(dim) unless given; window >
+    0: only the last `window` keys.  Returns out [T, n_heads, dim] of q's type,
+    or float32 with out_dtype; lse (float32 [T, n_heads]) is filled when given."""
+    torch = _torch()
+    T, n_heads, dim = q.shape
+    kv = _paged_kv(k_cache, v_cache)
+    b = _batch(cu_q, ctx_len, page_table, T, max_q)
+    _need(q.dtype == k_cache.dtype and q.stride(2) == 1 and q.stride(1) == dim and dim == kv.head_dim,
+          "q: [T, n_heads, dim] of the cache type, heads contiguous")
+    if out is None:
+        out = torch.empty((T, n_heads, dim), dtype=out_dtype or q.dtype, device=q.device)
+    _need(out.shape == q.shape and out.stride(2) == 1 and out.stride(1) == dim, "out: [T, n_heads, dim]")
+    _need(lse is None or (lse.shape == (T, n_heads) and lse.dtype == torch.float32 and lse.is_contiguous()),
+          "lse: float32 [T, n_heads]")
+    _on_gpu(q, k_cache, v_cache, cu_q, ctx_len, page_table, out, lse, ws)
+    L = lib()
+    if ws is None:
+        nbytes = L.moex_paged_attention_workspace_bytes(ctypes.byref(kv), ctypes.byref(b), n_heads)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    _check(L.moex_paged_attention(q.data_ptr(), q.stride(0) if T > 1 else n_heads * dim, ctypes.byref(kv),
+                                  ctypes.byref(b), n_heads, dim ** -0.5 if scale is None else scale, window,
+                                  out.data_ptr(), _type(out.dtype), out.stride(0) if T > 1 else n_heads * dim,
+                                  None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+                                  0 if ws is None else ws.numel(), _stream(stream)), "moex_paged_attention")
     return out
 
 

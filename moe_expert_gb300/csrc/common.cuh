@@ -24,6 +24,7 @@ enum : uint32_t {
   DEV_TIMEOUT_PIPE = 2u,               // an mbarrier wait of a copy pipeline ran out
   DEV_TIMEOUT_MMA = 4u,                // a tensor-core / TMEM wait ran out
   DEV_BAD_SHAPE = 8u,                  // a shape the kernel cannot take reached it
+  DEV_BAD_BATCH = 16u,                 // a batch's lengths, page ids or positions out of range
 };
 
 // Every bounded wait gives up after this many nanoseconds of %globaltimer.

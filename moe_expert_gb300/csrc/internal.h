@@ -84,4 +84,21 @@ size_t dense_prefill_ws_bytes(int T, int64_t rows, int64_t K);
 moex_status launch_dense_prefill(const moex_qweight* W, const uint16_t* x, int T, float* y, int64_t ldy, void* ws,
                                  cudaStream_t s);
 
+// The operators around the products (arguments checked in layer_api.cu).
+moex_status launch_add_rms_norm(const void* x, int x_type, int64_t ldx, const float* residual, int64_t ldr,
+                                const float* gamma, float eps, int T, int64_t H, float* sum, int64_t lds, void* y,
+                                int y_type, int64_t ldy, int8_t* q, float* ds, cudaStream_t s);
+moex_status launch_dequantize_q8_1(const int8_t* q, const float* ds, int T, int64_t K, void* y, int y_type,
+                                   cudaStream_t s);
+moex_status launch_route_experts(const void* logits, int type, int64_t ldl, const float* bias, int T, int E, int k,
+                                 int score, int groups, int top_groups, int group_top, int renorm, float scale,
+                                 int32_t* ids, float* w, cudaStream_t s);
+moex_status launch_rope_kv_write(const void* qkv, int type, int64_t ld, const moex_paged_kv* kv,
+                                 const moex_batch* batch, int n_heads, const float* cos_sin, int64_t n_pos,
+                                 int rot_dim, int interleaved, void* q, int64_t ldq, cudaStream_t s);
+size_t paged_attention_ws_bytes(const moex_paged_kv* kv, const moex_batch* batch, int n_heads);
+moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
+                                   int n_heads, float scale, int window, void* out, int out_type, int64_t ldo,
+                                   float* lse, void* ws, cudaStream_t s);
+
 }  // namespace moex

@@ -1,0 +1,118 @@
+// New tokens into a paged cache: rotary embedding of queries and keys, keys
+// and values to their slots, queries to a packed buffer.
+#include "batch.cuh"
+#include "internal.h"
+#include "rows.cuh"
+
+namespace moex {
+
+struct KvWriteArgs {
+  BatchView b;
+  const void* qkv;
+  const float* cos_sin;
+  void* q;
+  void* k;
+  void* v;
+  int64_t ld, ldq;
+  int n_heads, n_kv_heads, D, rot, interleaved, n_pos;
+};
+
+// One CTA a token; a thread takes 16 features of a head at a time.  In the
+// half-split form those are features j .. j+7 and j + rot/2 .. j + rot/2 + 7,
+// so a pair's two members meet in one thread; otherwise 16 in a row.
+template <int TYPE, int CT>
+__global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tok = blockIdx.x;
+  const int b = seq_of_token(a.b, tok);
+  int pos = -1, page = -1;
+  bool bad = b < 0;
+  if (b >= 0) {
+    const SeqView s = seq_view(a.b, b);
+    pos = s.ctx - s.n + (tok - s.first);
+    bad = s.bad || (a.rot > 0 && pos >= a.n_pos);
+    if (bad) pos = -1;
+    if (pos >= 0) page = page_of(a.b, b, pos);
+  }
+  if (bad && threadIdx.x == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+
+  const int per_head = a.D >> 4, rot_units = a.rot >> 4, half = a.rot >> 1;
+  const int units = (a.n_heads + 2 * a.n_kv_heads) * per_head;
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    const int h = u / per_head, j = u - h * per_head;
+    const bool is_q = h < a.n_heads, is_v = h >= a.n_heads + a.n_kv_heads;
+    if (!is_q && page < 0) continue;
+    const bool turn = !is_v && j < rot_units;
+    // feature offsets of the two groups of eight
+    const bool split = j < rot_units && !a.interleaved;
+    const int i0 = split ? 8 * j : 16 * j;
+    const int i1 = split ? half + 8 * j : 16 * j + 8;
+    float x[8], y[8];
+    if (pos >= 0) {
+      load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i0, x);
+      load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i1, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+    }
+    if (turn && pos >= 0) {
+      float c[8], s[8];
+      load8<MOEX_F32>(a.cos_sin, static_cast<int64_t>(pos) * a.rot + 8 * j, c);
+      load8<MOEX_F32>(a.cos_sin, static_cast<int64_t>(pos) * a.rot + half + 8 * j, s);
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = x[2 * i], r = x[2 * i + 1], p2 = y[2 * i], r2 = y[2 * i + 1];
+          x[2 * i] = p * c[i] - r * s[i];
+          x[2 * i + 1] = r * c[i] + p * s[i];
+          y[2 * i] = p2 * c[4 + i] - r2 * s[4 + i];
+          y[2 * i + 1] = r2 * c[4 + i] + p2 * s[4 + i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = x[i], r = y[i];
+          x[i] = p * c[i] - r * s[i];
+          y[i] = r * c[i] + p * s[i];
+        }
+      }
+    }
+    void* dst;
+    int64_t off;
+    if (is_q) {
+      dst = a.q;
+      off = tok * a.ldq + static_cast<int64_t>(h) * a.D;
+    } else {
+      const int hk = is_v ? h - a.n_heads - a.n_kv_heads : h - a.n_heads;
+      dst = is_v ? a.v : a.k;
+      off = kv_offset(a.b, page, hk, pos);
+    }
+    store8<CT>(dst, off + i0, x);
+    store8<CT>(dst, off + i1, y);
+  }
+}
+
+template <int TYPE>
+static cudaError_t write_launch(const KvWriteArgs& a, int ct, cudaStream_t s) {
+  const int units = (a.n_heads + 2 * a.n_kv_heads) * (a.D / 16);
+  const dim3 grid(a.b.n_tokens), block(units < 256 ? (units + 31) / 32 * 32 : 256);
+  return ct == MOEX_BF16 ? launch_pdl(kv_write_kernel<TYPE, MOEX_BF16>, grid, block, 0, s, a)
+                         : launch_pdl(kv_write_kernel<TYPE, MOEX_F16>, grid, block, 0, s, a);
+}
+
+moex_status launch_rope_kv_write(const void* qkv, int type, int64_t ld, const moex_paged_kv* kv,
+                                 const moex_batch* batch, int n_heads, const float* cos_sin, int64_t n_pos,
+                                 int rot_dim, int interleaved, void* q, int64_t ldq, cudaStream_t s) {
+  uint32_t* status = device_status_ptr();
+  if (!status) return MOEX_ECUDA;
+  const KvWriteArgs a{batch_view(kv, batch, status), qkv, cos_sin, q, kv->k, kv->v, ld, ldq, n_heads, kv->n_kv_heads,
+                      kv->head_dim, rot_dim, interleaved, static_cast<int>(n_pos)};
+  switch (type) {
+    case MOEX_BF16: return cuda_status(write_launch<MOEX_BF16>(a, kv->type, s));
+    case MOEX_F16: return cuda_status(write_launch<MOEX_F16>(a, kv->type, s));
+    default: return cuda_status(write_launch<MOEX_F32>(a, kv->type, s));
+  }
+}
+
+}  // namespace moex

@@ -26,9 +26,10 @@ Modules:
   gemv     -- per-block integer dots, the multi-column GEMV, its error bound
   moe      -- top-k routing, SwiGLU, the grouped MoE decode layer
   prefill  -- FP16 roundings, expert sort, the grouped MoE prefill layer
+  layer    -- norm, general expert routing, rotary cache write, paged attention
 
 Every function states which passage it follows.  Every function is pinned by
 the ``-m "not gpu"`` tests in ``tests/test_oracle_*.py`` against closed forms,
 brute force on tiny inputs and hand-derived fixtures under ``tests/golden/``.
 """
-from . import formats, q8_1, gemv, moe, prefill  # noqa: F401
+from . import formats, q8_1, gemv, moe, prefill, layer  # noqa: F401
