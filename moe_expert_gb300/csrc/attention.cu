@@ -1,94 +1,110 @@
-// Causal attention of new tokens over a paged cache.
-#include "batch.cuh"
+// Causal attention of new tokens over a paged cache: choice of the kernel, its
+// workspace, and the joining of tiles that several CTAs worked on.
+#include "attn.cuh"
+#include "attn_launch.h"
 #include "internal.h"
-#include "rows.cuh"
 
 namespace moex {
 
-struct AttnArgs {
-  BatchView b;
-  const void* q;
-  const void* k;
-  const void* v;
-  void* out;
-  float* lse;  // or nullptr
-  int64_t ldq, ldo;
-  float scale;
-  int n_heads, group, window, out_f32;
-};
-
-// One warp a (token, query head): lane l holds features l*D/32 .. of q, of
-// each key and of the output, and walks the keys with a running maximum and sum.
-template <int CT, int D>
-__global__ void __launch_bounds__(128) attend_rows_kernel(const AttnArgs a) {
+// Tiles that ranges cut, one column of CTAs for each range that begins inside a
+// tile and is the first to do so: the partials in the order of their keys, FP32.
+// CTA c leaves its first tile in slot 2c when it begins inside it, and its last
+// in slot 2c + 1 when it does not finish it.
+template <int CT, int D, int MT>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a) {
+  const int n_cta = gridDim.x;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int P = D / 32;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<int64_t>(a.b.n_tokens) * a.n_heads) return;
-  const int tok = static_cast<int>(w / a.n_heads), h = static_cast<int>(w % a.n_heads), hk = h / a.group;
-  using E = RowElem<CT>;
-  using T = typename E::T;
-  const int b = seq_of_token(a.b, tok);
-  float q[P], o[P], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    q[i] = E::get(static_cast<const T*>(a.q)[tok * a.ldq + static_cast<int64_t>(h) * D + lane * P + i]);
-    o[i] = 0.f;
+  const RangeStart x = a.plan[blockIdx.x];
+  if (x.u == 0) return;  // begins with a tile, or has no units
+  const int64_t u0 = x.tile_u + x.u;
+  const int c0 = static_cast<int>(range_of(x.tile_u, x.W, n_cta));
+  if (range_begin(range_of(u0 - 1, x.W, n_cta), x.W, n_cta) > x.tile_u) return;  // an earlier range cut it first
+  const int c1 = static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta));
+  const SeqView s = seq_view(a.b, x.b);
+  const float* ml = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
+  constexpr int V = D / 4;
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < x.rows * V; i += gridDim.y * blockDim.x) {
+    const int r = i / V, c4 = 4 * (i % V);
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      if (range_begin(c, x.W, n_cta) == range_begin(c + 1, x.W, n_cta)) continue;  // no units, no partial
+      const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * MT + r;
+      const float2 p = *reinterpret_cast<const float2*>(ml + 2 * at);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + at * D + c4);
+      const float mn = fmaxf(m, p.x), ref = mn == -INFINITY ? 0.f : mn;
+      const float f0 = fast_exp2(m - ref), f1 = fast_exp2(p.x - ref);
+      m = mn;
+      l = l * f0 + p.y * f1;
+      acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
+      acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+    }
+    const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r, a.ldo, D) + c4, acc);
+    if (a.lse && c4 == 0)
+      a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
   }
-  SeqView s{0, 0, 0, true};
-  if (b >= 0) s = seq_view(a.b, b);
-  if (s.bad && lane == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-  const int pos = b >= 0 ? s.ctx - s.n + (tok - s.first) : -1;
-  for (int j = a.window > 0 ? max(pos - a.window + 1, 0) : 0; j <= pos; ++j) {
-    const int page = page_of(a.b, b, j);
-    if (page < 0) continue;
-    const int64_t off = kv_offset(a.b, page, hk, j) + lane * P;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) x += q[i] * E::get(static_cast<const T*>(a.k)[off + i]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= a.scale;
-    const float mn = fmaxf(m, x);
-    if (mn == -INFINITY) continue;
-    const float c = expf(m - mn), p = expf(x - mn);
-    l = l * c + p;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < P; ++i) o[i] = o[i] * c + p * E::get(static_cast<const T*>(a.v)[off + i]);
-  }
-  const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int64_t at = tok * a.ldo + static_cast<int64_t>(h) * D + lane * P + i;
-    if (a.out_f32)
-      static_cast<float*>(a.out)[at] = o[i] * inv;
-    else
-      static_cast<T*>(a.out)[at] = static_cast<T>(o[i] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[w] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
-size_t paged_attention_ws_bytes(const moex_paged_kv*, const moex_batch*, int) { return 0; }
+namespace {
+
+// CTAs of a launch and its workspace: their range starts, then two partial tiles each.
+struct AttnGrid {
+  int ctas, mt;
+  size_t plan_bytes, bytes;
+};
+
+AttnGrid grid_of(const moex_paged_kv* kv) {
+  AttnGrid g;
+  g.mt = STREAM_MT;
+  g.ctas = STREAM_CTAS_PER_SM * sm_count();
+  g.plan_bytes = (g.ctas * sizeof(RangeStart) + 255) / 256 * 256;
+  g.bytes = g.plan_bytes + static_cast<size_t>(2 * g.ctas) * g.mt * (kv->head_dim + 2) * 4;
+  return g;
+}
 
 template <int CT, int D>
-static cudaError_t attend_launch(const AttnArgs& a, cudaStream_t s) {
-  const int64_t warps = static_cast<int64_t>(a.b.n_tokens) * a.n_heads;
-  return launch_pdl(attend_rows_kernel<CT, D>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, s, a);
+cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
+  return launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, dim3(g.ctas), dim3(128), 0, s, a);
+}
+
+}  // namespace
+
+size_t paged_attention_ws_bytes(const moex_paged_kv* kv, const moex_batch*, int) {
+  return grid_of(kv).bytes;
 }
 
 moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
                                    int n_heads, float scale, int window, void* out, int out_type, int64_t ldo,
-                                   float* lse, void*, cudaStream_t s) {
+                                   float* lse, void* ws, cudaStream_t s) {
   uint32_t* status = device_status_ptr();
   if (!status) return MOEX_ECUDA;
-  const AttnArgs a{batch_view(kv, batch, status), q, kv->k, kv->v, out, lse, ldq, ldo, scale, n_heads,
-                   n_heads / kv->n_kv_heads, window, out_type == MOEX_F32};
+  const AttnGrid g = grid_of(kv);
+  const AttnArgs a{batch_view(kv, batch, status),
+                   q,
+                   kv->k,
+                   kv->v,
+                   out,
+                   lse,
+                   static_cast<RangeStart*>(ws),
+                   reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + g.plan_bytes),
+                   ldq,
+                   ldo,
+                   scale * 1.4426950408889634f,
+                   n_heads,
+                   kv->n_kv_heads,
+                   n_heads / kv->n_kv_heads,
+                   window,
+                   out_type == MOEX_F32};
+  const cudaError_t e = launch_attend_stream(a, kv->type, kv->head_dim, g.ctas, s);
+  if (e != cudaSuccess) return MOEX_ECUDA;
   if (kv->type == MOEX_BF16)
-    return cuda_status(kv->head_dim == 64 ? attend_launch<MOEX_BF16, 64>(a, s) : attend_launch<MOEX_BF16, 128>(a, s));
-  return cuda_status(kv->head_dim == 64 ? attend_launch<MOEX_F16, 64>(a, s) : attend_launch<MOEX_F16, 128>(a, s));
+    return cuda_status(kv->head_dim == 64 ? launch_join<MOEX_BF16, 64>(a, g, s)
+                                          : launch_join<MOEX_BF16, 128>(a, g, s));
+  return cuda_status(kv->head_dim == 64 ? launch_join<MOEX_F16, 64>(a, g, s)
+                                        : launch_join<MOEX_F16, 128>(a, g, s));
 }
 
 }  // namespace moex

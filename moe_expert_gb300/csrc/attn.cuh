@@ -1,0 +1,191 @@
+// What the paged attention kernels share: their arguments, the division of a
+// ragged batch into equal shares, and the joining of partial results.
+//
+// The new tokens of a sequence and the `group` query heads of one key head
+// make one list of n * group rows (row r: token r / group, head r % group), so
+// every key and value is read once for all of them.  Rows are cut into tiles of
+// MT, the keys a tile sees into units of UK, and all units of the batch, in the
+// order sequence, key head, tile, keys, into one contiguous range a CTA:
+// CTA c of G takes units floor(c W / G) .. floor((c+1) W / G) of W, whatever the
+// lengths.  A tile inside one range is finished by its CTA; one that crosses a
+// border leaves FP32 partials (unnormalised output, maximum, sum) in the
+// workspace, which a second kernel joins in the order of the keys.
+#pragma once
+
+#include "batch.cuh"
+#include "rows.cuh"
+
+namespace moex {
+
+// Where a CTA's range begins, for the kernel that joins the tiles cut there.
+struct RangeStart {
+  int64_t W, tile_u;     // units of the batch; units before the tile
+  int b, hk, t, u;       // sequence, key head, tile, unit inside the tile
+  int units, rows;       // of the tile
+};
+
+struct AttnArgs {
+  BatchView b;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;         // or nullptr
+  struct RangeStart* plan;  // [G]
+  float* part;        // [2 G][MT][D], then [2 G][MT][2]
+  int64_t ldq, ldo;
+  float scale_log2;   // scale * log2(e): scores are kept in powers of two
+  int n_heads, n_kv_heads, group, window, out_f32;
+};
+
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One tile of a sequence's rows and the keys that its rows see.
+struct Tile {
+  int r0, r1;  // rows
+  int lo, hi;  // keys [lo, hi); lo is a multiple of 16
+  int units;   // at least one, so that rows without keys are written too
+};
+
+template <int MT, int UK>
+__device__ __forceinline__ Tile tile_of(const SeqView& s, int group, int window, int t) {
+  Tile x;
+  x.r0 = t * MT;
+  x.r1 = min(s.n * group, x.r0 + MT);
+  const int base = s.ctx - s.n;
+  x.hi = max(base + (x.r1 - 1) / group + 1, 0);
+  x.lo = window > 0 ? max(base + x.r0 / group - window + 1, 0) & ~15 : 0;
+  x.lo = min(x.lo, x.hi & ~15);
+  x.units = max((x.hi - x.lo + UK - 1) / UK, 1);
+  return x;
+}
+
+template <int MT, int UK>
+__device__ __forceinline__ int64_t seq_units(const SeqView& s, int group, int window) {
+  const int tiles = (s.n * group + MT - 1) / MT;
+  int64_t u = 0;
+  for (int t = 0; t < tiles; ++t) u += tile_of<MT, UK>(s, group, window, t).units;
+  return u;
+}
+
+__host__ __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t W, int64_t G) { return c * W / G; }
+// The CTA whose range holds unit u.
+__host__ __device__ __forceinline__ int64_t range_of(int64_t u, int64_t W, int64_t G) { return ((u + 1) * G - 1) / W; }
+
+// Where a CTA is in the list of units.
+struct Cursor {
+  int64_t left;    // units of this CTA's range still to do, from here on
+  int b, hk, t, u; // sequence, key head, tile, unit inside the tile
+  SeqView s;
+  Tile x;
+};
+
+// Every CTA finds the batch's number of units and its own range: a scan over
+// the sequences, THREADS at a time.  The cursor is at the range's first unit,
+// and so is the CTA's entry of the plan.
+template <int MT, int UK, int THREADS>
+__device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
+  __shared__ int64_t warp_sum[2][THREADS / 32];
+  __shared__ int64_t found[2];  // sequence, units before it
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t total = 0, mine = 0, before = 0;
+  // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
+  for (int pass = 0; pass < 2; ++pass) {
+    const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
+    int64_t run = 0;
+    for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
+      const int b = base + threadIdx.x;
+      if (pass == 0 || a.b.n_seqs > THREADS) {
+        int64_t v = 0;
+        if (b < a.b.n_seqs) {
+          const SeqView s = seq_view(a.b, b);
+          if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+          v = s.n > 0 ? a.n_kv_heads * seq_units<MT, UK>(s, a.group, a.window) : 0;
+        }
+        mine = v;
+        int64_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sum[it & 1][warp] = x;
+        __syncthreads();
+        before = run;
+        for (int w = 0; w < THREADS / 32; ++w) {
+          const int64_t ws = warp_sum[it & 1][w];
+          if (w < warp) before += ws;
+          run += ws;
+        }
+        before += x - v;
+      }
+      if (pass == 1 && mine > 0 && before <= want && want < before + mine) {
+        found[0] = b;
+        found[1] = before;
+      }
+    }
+    if (pass == 0) total = run;
+    __syncthreads();
+  }
+  const int64_t u0 = range_begin(cta, total, n_cta);
+  cur.left = range_begin(cta + 1, total, n_cta) - u0;
+  if (cur.left == 0) {
+    if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0};
+    return;
+  }
+  cur.b = static_cast<int>(found[0]);
+  cur.s = seq_view(a.b, cur.b);
+  int64_t off = u0 - found[1];
+  const int64_t per = seq_units<MT, UK>(cur.s, a.group, a.window);
+  cur.hk = static_cast<int>(off / per);
+  off -= cur.hk * per;
+  for (cur.t = 0;; ++cur.t) {
+    cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
+    if (off < cur.x.units) break;
+    off -= cur.x.units;
+  }
+  cur.u = static_cast<int>(off);
+  if (threadIdx.x == 0)
+    a.plan[cta] = RangeStart{total, u0 - off, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0};
+}
+
+// To the first unit of the next tile; `done` units of this one were in the range.
+template <int MT, int UK>
+__device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int done) {
+  cur.left -= done;
+  cur.u = 0;
+  if (cur.left <= 0) return;
+  ++cur.t;
+  if (cur.t * MT >= cur.s.n * a.group) {
+    cur.t = 0;
+    if (++cur.hk == a.n_kv_heads) {
+      cur.hk = 0;
+      do {
+        cur.s = seq_view(a.b, ++cur.b);
+      } while (cur.s.n == 0);
+    }
+  }
+  cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
+}
+
+// Offset of row r of a tile's sequence and key head in a packed [token][head][D] buffer.
+__device__ __forceinline__ int64_t row_offset(const SeqView& s, int group, int hk, int r, int64_t ld, int D) {
+  const int i = r / group;
+  return (s.first + i) * ld + static_cast<int64_t>(hk * group + (r - i * group)) * D;
+}
+
+template <int CT>
+__device__ __forceinline__ void store_out4(const AttnArgs& a, int64_t off, float4 v) {
+  if (a.out_f32)
+    store4<MOEX_F32>(a.out, off, v);
+  else
+    store4<CT>(a.out, off, v);
+}
+
+}  // namespace moex

@@ -1,0 +1,15 @@
+// Tile sizes and launchers of the paged attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace moex {
+
+struct AttnArgs;
+
+// Few rows a key head: tiles of 16 rows, units of 64 keys, two CTAs an SM.
+constexpr int STREAM_MT = 16, STREAM_UK = 64, STREAM_CTAS_PER_SM = 2;
+
+cudaError_t launch_attend_stream(const AttnArgs& a, int type, int D, int ctas, cudaStream_t s);
+
+}  // namespace moex

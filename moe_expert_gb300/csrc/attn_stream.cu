@@ -1,0 +1,297 @@
+// Paged attention for few rows a key head (single tokens, drafts): the cache
+// is streamed once, so DRAM bounds it.
+//
+// A CTA of four warps works on one tile of 16 rows; each warp runs alone
+// over every fourth step of 16 keys, with its own ring of copies in flight
+// (cp.async, no CTA barrier in the loop), its own running maximum and sum, and
+// the products on mma.sync m16n8k16: with 16 rows a step of 16 keys is 8 KB of
+// cache and 32 such instructions, far below the tensor rate, and tcgen05's
+// 128-row tiles would be mostly empty.  The four warps' results meet in shared
+// memory at the end of a tile.
+#include "attn.cuh"
+#include "attn_launch.h"
+#include "internal.h"
+
+namespace moex {
+namespace {
+
+constexpr int MT = STREAM_MT, UK = STREAM_UK;
+constexpr int WARPS = 4, STEP = 16, STAGES = 3;
+static_assert(UK == WARPS * STEP, "a unit is one step of every warp");
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <int CT>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (CT == MOEX_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Shared memory: the rings (warp, stage, K then V), reused at the end of a
+// tile for the warps' outputs [WARPS][MT][D + 4] and their maxima and sums.
+template <int D>
+struct Smem {
+  static constexpr int PLANE = STEP * D * 2;   // bytes of a step's keys
+  static constexpr int RING = WARPS * STAGES * 2 * PLANE;
+  static constexpr int PITCH = D + 4;          // floats of an output row
+  static constexpr int JOIN = WARPS * MT * (PITCH + 2) * 4;
+  static constexpr int BYTES = RING > JOIN ? RING : JOIN;
+};
+
+template <int CT, int D>
+__global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArgs a) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  using S = Smem<D>;
+  using E = RowElem<CT>;
+  constexpr int CH = D / 8;     // 16-byte chunks of a row
+  constexpr int KS = D / 16;    // k-steps of the first product
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, p2 = 2 * (lane & 3);
+  pdl_wait();
+  Cursor cur;
+  find_range<MT, UK, WARPS * 32>(a, blockIdx.x, gridDim.x, cur);
+  const uint32_t ring = smem_u32(sm) + warp * STAGES * 2 * S::PLANE;
+
+  while (cur.left > 0) {
+    const Tile x = cur.x;
+    const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(x.units - cur.u)));
+    const int first = x.lo + cur.u * UK;  // this CTA's keys of the tile
+    const int end = min(x.hi, first + units * UK);
+    const int base = cur.s.ctx - cur.s.n;
+
+    // Q as the A operand: rows g and g + 8, the same for every step
+    uint32_t qf[KS][4];
+    int top[2], bot[2];  // keys bot < j <= top are seen by the row
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = x.r0 + g + 8 * half;
+      const bool in = r < x.r1;
+      top[half] = in ? base + r / a.group : -1;
+      bot[half] = a.window > 0 ? top[half] - a.window : -1;
+      const uint16_t* row =
+          static_cast<const uint16_t*>(a.q) + (in ? row_offset(cur.s, a.group, cur.hk, r, a.ldq, D) : 0);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        qf[i][half] = in ? *reinterpret_cast<const uint32_t*>(row + 16 * i + p2) : 0u;
+        qf[i][2 + half] = in ? *reinterpret_cast<const uint32_t*>(row + 16 * i + 8 + p2) : 0u;
+      }
+    }
+
+    // steps of this warp: keys k0 + i * UK .. + 15
+    const int k0 = first + warp * STEP;
+    const int steps = end > k0 ? (end - k0 + UK - 1) / UK : 0;
+    // lane l holds the pages of step 32 * (i / 32) + l: its first and its second eight keys
+    int pg0 = -1, pg1 = -1;
+    const int32_t* table = a.b.table + cur.b * a.b.table_stride;
+    auto fetch_pages = [&](int i) {
+      const int j = k0 + (i + lane) * UK;
+      pg0 = pg1 = -1;
+      if (j < end) {
+        pg0 = table[j >> a.b.page_shift];
+        pg1 = j + 8 < end ? table[(j + 8) >> a.b.page_shift] : pg0;
+        if (pg0 < 0 || pg0 >= a.b.n_pages || pg1 < 0 || pg1 >= a.b.n_pages) {
+          flag_status(a.b.status, DEV_BAD_BATCH);
+          if (pg0 < 0 || pg0 >= a.b.n_pages) pg0 = -1;
+          if (pg1 < 0 || pg1 >= a.b.n_pages) pg1 = -1;
+        }
+      }
+    };
+    uint32_t ok_ring = 0;  // two bits a stage: the step's halves have a page
+    auto load = [&](int i, int stage) {
+      if (i < steps) {
+        if ((i & 31) == 0) fetch_pages(i);
+        const int j = k0 + i * UK;
+        const int a0 = __shfl_sync(0xffffffffu, pg0, i & 31), a1 = __shfl_sync(0xffffffffu, pg1, i & 31);
+        ok_ring = (ok_ring & ~(3u << (2 * stage))) | ((a0 >= 0 ? 1u : 0u) | (a1 >= 0 ? 2u : 0u)) << (2 * stage);
+        const uint32_t dst = ring + stage * 2 * S::PLANE;
+        constexpr int RPI = 32 / CH;  // rows an instruction covers
+        const int c = lane % CH;
+#pragma unroll
+        for (int n = 0; n < STEP / RPI; ++n) {
+          const int r = n * RPI + lane / CH;
+          const int page = r < 8 ? a0 : a1;
+          const bool in = j + r < end && page >= 0;
+          const int64_t off = in ? kv_offset(a.b, page, cur.hk, j + r) + 8 * c : 0;
+          const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
+          cp_async16(at, static_cast<const uint16_t*>(a.k) + off, in ? 16u : 0u);
+          cp_async16(at + S::PLANE, static_cast<const uint16_t*>(a.v) + off, in ? 16u : 0u);
+        }
+      }
+      cp_commit();
+    };
+
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) load(i, i);
+    int stage = 0;
+    for (int i = 0; i < steps; ++i) {
+      cp_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies have landed, and the stage refilled next has been read
+      load(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t kb = ring + stage * 2 * S::PLANE, vb = kb + S::PLANE;
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        const int r = (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t f[4];
+          ldsm4(f, kb + r * (D * 2) + (((2 * ks + c) ^ (r & 7)) << 4));
+          mma16816<CT>(s[0], qf[ks], f[0], f[1]);
+          mma16816<CT>(s[1], qf[ks], f[2], f[3]);
+        }
+      }
+      const int j = k0 + i * UK;
+      const uint32_t ok = (ok_ring >> (2 * stage)) & 3u;
+      float mx[2] = {m[0], m[1]};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int half = e >> 1, key = j + 8 * nt + p2 + (e & 1);
+          const bool seen = key <= top[half] && key > bot[half] && ((ok >> nt) & 1u);
+          s[nt][e] = seen ? s[nt][e] * a.scale_log2 : -INFINITY;
+          mx[half] = fmaxf(mx[half], s[nt][e]);
+        }
+      float corr[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
+        mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+        // a row that has seen no key keeps 0 as its reference, so that -inf - -inf does not arise
+        const float ref = mx[half] == -INFINITY ? 0.f : mx[half];
+        corr[half] = fast_exp2(m[half] - ref);
+        m[half] = mx[half];
+        l[half] *= corr[half];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float pv = fast_exp2(s[nt][2 * half + e] - ref);
+            s[nt][2 * half + e] = pv;
+            l[half] += pv;
+          }
+      }
+      // probabilities rounded to the cache type: the A operand of the second product
+      const uint32_t pf[4] = {E::pack(s[0][0], s[0][1]), E::pack(s[0][2], s[0][3]), E::pack(s[1][0], s[1][1]),
+                              E::pack(s[1][2], s[1][3])};
+      {
+        const int r = ((lane >> 3) & 1) * 8 + (lane & 7), c = lane >> 4;
+#pragma unroll
+        for (int nt = 0; nt < D / 16; ++nt) {
+          uint32_t f[4];
+          ldsm4_t(f, vb + r * (D * 2) + (((2 * nt + c) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float(&od)[4] = o[2 * nt + h];
+            od[0] *= corr[0], od[1] *= corr[0], od[2] *= corr[1], od[3] *= corr[1];
+            mma16816<CT>(od, pf, f[2 * h], f[2 * h + 1]);
+          }
+        }
+      }
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+    }
+    __syncthreads();  // every warp is done with its ring
+    float* jo = reinterpret_cast<float*>(sm);
+    float* jm = jo + WARPS * MT * S::PITCH;  // [WARPS][MT][2]
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = g + 8 * half;
+      if (x.r0 + r < x.r1) {
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt)
+          *reinterpret_cast<float2*>(jo + (warp * MT + r) * S::PITCH + 8 * nt + p2) =
+              make_float2(o[nt][2 * half], o[nt][2 * half + 1]);
+        if ((lane & 3) == 0)
+          *reinterpret_cast<float2*>(jm + (warp * MT + r) * 2) = make_float2(m[half], l[half]);
+      }
+    }
+    __syncthreads();
+    const bool whole = units == x.units;
+    const int slot = 2 * blockIdx.x + (cur.u == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < (x.r1 - x.r0) * (D / 4); i += WARPS * 32) {
+      const int r = i / (D / 4), c = 4 * (i % (D / 4));
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, jm[(w * MT + r) * 2]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 ml = *reinterpret_cast<const float2*>(jm + (w * MT + r) * 2);
+        const float f = fast_exp2(ml.x - ref);
+        const float4 v = *reinterpret_cast<const float4*>(jo + (w * MT + r) * S::PITCH + c);
+        ll += f * ml.y;
+        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+      }
+      if (whole) {
+        const float inv = ll > 0.f ? __fdiv_rn(1.f, ll) : 0.f;
+        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+        store_out4<CT>(a, row_offset(cur.s, a.group, cur.hk, x.r0 + r, a.ldo, D) + c, acc);
+        if (a.lse && c == 0)
+          a.lse[row_offset(cur.s, a.group, cur.hk, x.r0 + r, a.n_heads, 1)] =
+              ll > 0.f ? mm * LN2 + logf(ll) : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * MT + r) * D + c) = acc;
+        if (c == 0) {
+          float* ml = a.part + static_cast<int64_t>(2 * gridDim.x) * MT * D + (static_cast<int64_t>(slot) * MT + r) * 2;
+          ml[0] = mm;
+          ml[1] = ll;
+        }
+      }
+    }
+    __syncthreads();  // the ring is free again
+    next_tile<MT, UK>(a, cur, units);
+  }
+  pdl_launch_dependents();
+}
+
+template <int CT, int D>
+cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attend_stream_kernel<CT, D>), Smem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_stream_kernel<CT, D>, dim3(ctas), dim3(WARPS * 32), Smem<D>::BYTES, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_stream(const AttnArgs& a, int type, int D, int ctas, cudaStream_t s) {
+  if (type == MOEX_BF16) return D == 64 ? launch<MOEX_BF16, 64>(a, ctas, s) : launch<MOEX_BF16, 128>(a, ctas, s);
+  return D == 64 ? launch<MOEX_F16, 64>(a, ctas, s) : launch<MOEX_F16, 128>(a, ctas, s);
+}
+
+}  // namespace moex
