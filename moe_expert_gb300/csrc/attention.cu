@@ -52,14 +52,16 @@ namespace {
 
 // CTAs of a launch and its workspace: their range starts, then two partial tiles each.
 struct AttnGrid {
+  bool tile;  // the tcgen05 kernel of 256-row tiles
   int ctas, mt;
   size_t plan_bytes, bytes;
 };
 
-AttnGrid grid_of(const moex_paged_kv* kv) {
+AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads) {
   AttnGrid g;
-  g.mt = STREAM_MT;
-  g.ctas = STREAM_CTAS_PER_SM * sm_count();
+  g.tile = static_cast<int64_t>(b->max_q) * (n_heads / kv->n_kv_heads) > TILE_MIN_ROWS;
+  g.mt = g.tile ? TILE_MT : STREAM_MT;
+  g.ctas = (g.tile ? 1 : STREAM_CTAS_PER_SM) * sm_count();
   g.plan_bytes = (g.ctas * sizeof(RangeStart) + 255) / 256 * 256;
   g.bytes = g.plan_bytes + static_cast<size_t>(2 * g.ctas) * g.mt * (kv->head_dim + 2) * 4;
   return g;
@@ -67,13 +69,14 @@ AttnGrid grid_of(const moex_paged_kv* kv) {
 
 template <int CT, int D>
 cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
+  if (g.tile) return launch_pdl(attend_join_kernel<CT, D, TILE_MT>, dim3(g.ctas, 8), dim3(128), 0, s, a);
   return launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, dim3(g.ctas), dim3(128), 0, s, a);
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(const moex_paged_kv* kv, const moex_batch*, int) {
-  return grid_of(kv).bytes;
+size_t paged_attention_ws_bytes(const moex_paged_kv* kv, const moex_batch* batch, int n_heads) {
+  return grid_of(kv, batch, n_heads).bytes;
 }
 
 moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
@@ -81,7 +84,7 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                                    float* lse, void* ws, cudaStream_t s) {
   uint32_t* status = device_status_ptr();
   if (!status) return MOEX_ECUDA;
-  const AttnGrid g = grid_of(kv);
+  const AttnGrid g = grid_of(kv, batch, n_heads);
   const AttnArgs a{batch_view(kv, batch, status),
                    q,
                    kv->k,
@@ -98,7 +101,8 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                    n_heads / kv->n_kv_heads,
                    window,
                    out_type == MOEX_F32};
-  const cudaError_t e = launch_attend_stream(a, kv->type, kv->head_dim, g.ctas, s);
+  const cudaError_t e = g.tile ? launch_attend_tile(a, kv->type, kv->head_dim, g.ctas, s)
+                               : launch_attend_stream(a, kv->type, kv->head_dim, g.ctas, s);
   if (e != cudaSuccess) return MOEX_ECUDA;
   if (kv->type == MOEX_BF16)
     return cuda_status(kv->head_dim == 64 ? launch_join<MOEX_BF16, 64>(a, g, s)

@@ -1,0 +1,449 @@
+// Paged attention for many rows a key head (prompts and chunks) on tcgen05.
+//
+// A CTA (one an SM) works on a tile of 256 rows as two groups of 128, over
+// blocks of 128 keys.  With S = Q K^T and O = P V:
+//   - S of a group: 128 x 128 FP32 in TMEM; P (16-bit) replaces it in place and
+//     is the A operand of the second product, so neither touches shared memory;
+//   - O of a group: 128 x D FP32 in TMEM.  4 * 128 columns hold both groups.
+// Both groups use one copy of every key block: 64 KB of cache feed 4 products of
+// 128 x 128 x 128.
+// Warps: 0-3 copy keys and values (cp.async: pages may be as short as eight
+// keys, which as TMA boxes would be 2 KB each and bound by the box rate),
+// 4-7 and 8-11 the softmax of the two groups, one row a thread, so maxima and
+// sums need no exchange; 12 issues the MMAs; 13-15 copy Q.
+// The MMA order is PV0(j), QK0(j+1), PV1(j), QK1(j+1): while one group's
+// products run the other's softmax does.  A row's reference for the exponentials
+// follows its maximum only when that grows by more than 2^8, so O is rescaled
+// rarely; sums and O are exact for any reference.
+#include "attn.cuh"
+#include "attn_launch.h"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace moex {
+namespace {
+
+constexpr int MT = TILE_MT, UK = TILE_UK;
+constexpr int THREADS = 512;
+constexpr float GROW = 8.f;  // log2 of the growth of a maximum that rescales O
+
+template <int D>
+struct Lay {
+  static constexpr int HALF = 128 * 128;              // 128 rows of 64 elements, 128-byte swizzle
+  static constexpr int STAGE = (D / 64) * HALF;       // 128 keys (or values)
+  static constexpr int NS = D == 64 ? 8 : 5;          // stages: K0 V0 K1 V1 ...
+  static constexpr int Q = 0;                         // [group][half]
+  static constexpr int RING = 2 * STAGE;
+  static constexpr int BARS = RING + NS * STAGE;
+  static constexpr int N_BARS = 2 * NS + 2 + 8 + 1;
+  static constexpr int BYTES = BARS + N_BARS * 8 + 16;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Shared-memory writes of this thread before reads by the tensor core.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+template <int R>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int CT, int D>
+__global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  using L = Lay<D>;
+  using E = RowElem<CT>;
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  constexpr int NS = L::NS;
+  __shared__ uint32_t tmem_holder;
+  __shared__ int abort_word;
+  __shared__ Cursor cursors[THREADS / 32];  // every warp walks the range by itself; not kept in its registers
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + L::BARS);
+  uint64_t* kv_empty = kv_full + NS;
+  uint64_t* q_full = kv_empty + NS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_empty = o_full + 2;
+  uint64_t* done = o_empty + 2;
+
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 4);   // the four copying warps
+      mbar_init(&kv_empty[i], 1);  // a commit
+    }
+    mbar_init(q_full, 3);
+    mbar_init(q_empty, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&o_full[g], 1);
+      mbar_init(&o_empty[g], 4);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_holder, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  Cursor& cur = cursors[warp];
+  {
+    Cursor at;
+    find_range<MT, UK, THREADS>(a, blockIdx.x, gridDim.x, at);
+    if (lane == 0) cur = at;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  const uint32_t smb = smem_u32(sm);
+
+  // A wait of a whole warp: all of its lanes go on, or none.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity, uint32_t bit) {
+    if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) return true;
+    if (!*abort_flag) flag_status(a.b.status, bit);
+    *abort_flag = 1;
+    return false;
+  };
+  auto advance = [&](int units) {
+    __syncwarp();
+    if (lane == 0) next_tile<MT, UK>(a, cur, units);
+    __syncwarp();
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------ keys and values
+    regs_down<80>();
+    const int c = threadIdx.x % CH, r0 = threadIdx.x / CH;  // chunk, row within a group of RPI rows
+    constexpr int RPI = 128 / CH;                            // rows a round of the 128 threads covers: 8 or 16
+    const uint32_t dst0 = (c >> 3) * L::HALF + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
+    int n = 0, told = 0;  // stages issued, stages announced
+    auto announce = [&](int upto) {
+      fence_async_smem();
+      __syncwarp();
+      for (; told < upto; ++told)
+        if (lane == 0) mbar_arrive(&kv_full[told % NS]);
+    };
+    bool ok = true;
+    while (cur.left > 0 && ok) {
+      const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+      const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, b = cur.b, hk = cur.hk;
+      for (int i = 0; i < units && ok; ++i) {
+        const int j0 = first + i * UK;
+        // lane l < 16: the page of keys j0 + 8 l .. + 7
+        int pg = -1;
+        if (lane < 16 && j0 + 8 * lane < hi) pg = page_of(a.b, b, j0 + 8 * lane);
+        for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+          const int slot = n % NS;
+          if (n >= NS && !__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[slot], ((n / NS) - 1) & 1))) {
+            // about to wait: hand over everything that is under way first
+            cp_wait<0>();
+            announce(n);
+            ok = warp_wait(&kv_empty[slot], ((n / NS) - 1) & 1, DEV_TIMEOUT_PIPE);
+            if (!ok) break;
+          }
+          const uint32_t dst = smb + L::RING + slot * L::STAGE + dst0;
+          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.v : a.k) + 8 * c;
+#pragma unroll 4
+          for (int it = 0; it < 128 / RPI; ++it) {
+            const int r = it * RPI + r0, j = j0 + r;
+            const int page = __shfl_sync(0xffffffffu, pg, r >> 3);
+            const bool in = j < hi && page >= 0;
+            cp_async16(dst + it * RPI * 128, src + (in ? kv_offset(a.b, page, hk, j) : 0), in ? 16u : 0u);
+          }
+          cp_commit();
+          if (n >= 2) {
+            cp_wait<2>();
+            announce(n - 1);
+          }
+        }
+      }
+      advance(units);
+    }
+    cp_wait<0>();
+    if (ok) announce(n);
+  } else if (warp >= 12) {
+    regs_down<80>();
+    if (warp == 12) {
+      // ------------------------------------------------ MMA issue
+      if (lane == 0) {
+        constexpr uint32_t IDESC_S = idesc_16_f32(128, 128, CT == MOEX_BF16, false);
+        constexpr uint32_t IDESC_O = idesc_16_f32(128, D, CT == MOEX_BF16, true);
+        const uint64_t qd = smem_desc_sw128(smb + L::Q);
+        const uint64_t kd = smem_desc_sw128(smb + L::RING);
+        const uint64_t vd = smem_desc_mn_sw128(smb + L::RING, L::HALF);
+        int n = 0, tile = 0;
+        int np[2] = {0, 0}, no[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, abort_flag)) {
+            if (!*abort_flag) flag_status(a.b.status, DEV_TIMEOUT_MMA);
+            *abort_flag = 1;
+            ok = false;
+          }
+          return ok;
+        };
+        auto first = [&](int g, int slot) {  // S_g = Q_g K^T
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4;
+            mma_f16_ss(tmem + g * 128, qd + ((g * L::STAGE) >> 4) + off, kd + ((slot * L::STAGE) >> 4) + off, IDESC_S,
+                       ks != 0);
+          }
+        };
+        auto second = [&](int g, int slot, bool acc) {  // O_g (+)= P_g V
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * ks, vd + ((slot * L::STAGE + ks * 2048) >> 4), IDESC_O,
+                       acc || ks != 0);
+        };
+        while (cur.left > 0 && ok) {
+          const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+          const int groups = cur.x.r1 - cur.x.r0 > 128 ? 2 : 1;
+          if (!wait(q_full, tile & 1)) break;
+          if (!wait(&kv_full[n % NS], (n / NS) & 1)) break;
+          tc_fence_after();
+          for (int g = 0; g < groups; ++g) {
+            first(g, n % NS);
+            mma_commit(&s_full[g]);
+          }
+          mma_commit(&kv_empty[n % NS]);
+          if (units == 1) mma_commit(q_empty);
+          for (int i = 0; i < units && ok; ++i, n += 2) {
+            const int vs = (n + 1) % NS, ks = (n + 2) % NS;
+            if (!wait(&kv_full[vs], ((n + 1) / NS) & 1)) break;
+            for (int g = 0; g < groups && ok; ++g) {
+              if (i == 0 && no[g] > 0 && !wait(&o_empty[g], (no[g] - 1) & 1)) break;
+              if (!wait(&p_full[g], np[g] & 1)) break;
+              ++np[g];
+              tc_fence_after();
+              second(g, vs, i > 0);
+              if (g == groups - 1) mma_commit(&kv_empty[vs]);
+              if (i + 1 < units) {
+                if (g == 0 && !wait(&kv_full[ks], ((n + 2) / NS) & 1)) break;
+                tc_fence_after();
+                first(g, ks);
+                mma_commit(&s_full[g]);
+                if (g == groups - 1) {
+                  mma_commit(&kv_empty[ks]);
+                  if (i + 2 == units) mma_commit(q_empty);
+                }
+              } else {
+                mma_commit(&o_full[g]);
+                ++no[g];
+              }
+            }
+          }
+          ++tile;
+          next_tile<MT, UK>(a, cur, units);  // this lane alone
+        }
+        // the CTA leaves its TMEM and shared memory only when nothing reads them any more
+        mma_commit(done);
+        mbar_wait(done, 0, nullptr);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------ queries
+      int tile = 0;
+      while (cur.left > 0) {
+        const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+        if (tile > 0 && !warp_wait(q_empty, (tile - 1) & 1, DEV_TIMEOUT_PIPE)) break;
+        const int rows = cur.x.r1 - cur.x.r0;
+#pragma unroll 2
+        for (int i = threadIdx.x - 13 * 32; i < (rows > 128 ? 256 : 128) * CH; i += 96) {
+          const int r = i / CH, c = i % CH;
+          const bool in = r < rows;
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                                (in ? row_offset(cur.s, a.group, cur.hk, cur.x.r0 + r, a.ldq, D) + 8 * c : 0);
+          cp_async16(smb + L::Q + (r >> 7) * L::STAGE + (c >> 3) * L::HALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     src, in ? 16u : 0u);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        ++tile;
+        advance(units);
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax
+    regs_up<176>();
+    const int g = (warp >> 2) - 1;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes 32 * (warp % 4)
+    const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
+    const int row = g * 128 + (warp & 3) * 32 + lane;
+    int ns = 0, no = 0;
+    bool ok = true;
+    while (cur.left > 0 && ok) {
+      const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+      if (cur.x.r1 - cur.x.r0 > g * 128) {
+        const int r = cur.x.r0 + row;
+        const bool in = r < cur.x.r1;
+        const int first = cur.x.lo + cur.u * UK, end = cur.x.hi;
+        const int32_t* table = a.b.table + cur.b * a.b.table_stride;
+        const int top = in ? cur.s.ctx - cur.s.n + r / a.group : -1;
+        const int bot = a.window > 0 ? top - a.window : -1;
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < units; ++i, ++ns) {
+          const int j0 = first + i * UK;
+          // keys without a page (lane c: keys j0 + 8 c .. + 7); read while the product runs
+          int pg = 0;
+          if (lane < 16 && j0 + 8 * lane < end) {
+            pg = table[(j0 + 8 * lane) >> a.b.page_shift];
+            pg = pg < 0 || pg >= a.b.n_pages;
+          }
+          const uint32_t bad = __ballot_sync(0xffffffffu, pg != 0);
+          ok = warp_wait(&s_full[g], ns & 1, DEV_TIMEOUT_MMA);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+          tmem_ld_wait();
+          // every key of the block seen by every row of the warp?
+          const bool clean = __all_sync(0xffffffffu, j0 + UK - 1 <= top && j0 > bot) && bad == 0;
+          if (!clean) {
+            const int hi = top - j0, lo = bot - j0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int c = 32 * q + e;
+                if (!(c <= hi && c > lo) || ((bad >> (c >> 3)) & 1u)) s[q][e] = 0xff800000u;  // -inf
+              }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+          const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          const bool grow = top_s > m + GROW || (i == 0 && top_s > m) || (m == -INFINITY && top_s > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? top_s : m;
+            const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+            m = mn;
+            l *= f;
+            if (i > 0) {
+#pragma unroll
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * q, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + 16 * q, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(s[q][2 * e]), a.scale_log2, -ref));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(s[q][2 * e + 1]), a.scale_log2, -ref));
+              sum[e & 1] += p0;
+              sum[2 + (e & 1)] += p1;
+              pk[e] = E::pack(p0, p1);
+            }
+            tmem_st16(ts + 16 * q, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
+        }
+        if (!ok) break;
+        // the tile's (or the range's) output
+        ok = warp_wait(&o_full[g], no & 1, DEV_TIMEOUT_MMA);
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+        const bool whole = units == cur.x.units;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u == 0 ? 1 : 0);
+        const float inv = whole ? (l > 0.f ? __fdiv_rn(1.f, l) : 0.f) : 1.f;
+        const int64_t off = in ? row_offset(cur.s, a.group, cur.hk, r, a.ldo, D) : 0;
+        float* part = a.part + (slot * MT + row) * D;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * q, o);
+          tmem_ld_wait();
+          if (q == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[g]);
+          }
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float v[8];
+#pragma unroll
+              for (int w = 0; w < 8; ++w) v[w] = __uint_as_float(o[e + w]) * inv;
+              if (!whole)
+                store8<MOEX_F32>(part, 32 * q + e, v);
+              else if (a.out_f32)
+                store8<MOEX_F32>(a.out, off + 32 * q + e, v);
+              else
+                store8<CT>(a.out, off + 32 * q + e, v);
+            }
+          }
+        }
+        if (in) {
+          if (!whole) {
+            float* ml = a.part + 2 * static_cast<int64_t>(gridDim.x) * MT * D + (slot * MT + row) * 2;
+            ml[0] = m;
+            ml[1] = l;
+          } else if (a.lse) {
+            a.lse[row_offset(cur.s, a.group, cur.hk, r, a.n_heads, 1)] =
+                l > 0.f ? m * LN2 + logf(l) : -INFINITY;
+          }
+        }
+      }
+      advance(units);
+    }
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int CT, int D>
+cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attend_tile_kernel<CT, D>), Lay<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_tile_kernel<CT, D>, dim3(ctas), dim3(THREADS), Lay<D>::BYTES, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tile(const AttnArgs& a, int type, int D, int ctas, cudaStream_t s) {
+  if (type == MOEX_BF16) return D == 64 ? launch<MOEX_BF16, 64>(a, ctas, s) : launch<MOEX_BF16, 128>(a, ctas, s);
+  return D == 64 ? launch<MOEX_F16, 64>(a, ctas, s) : launch<MOEX_F16, 128>(a, ctas, s);
+}
+
+}  // namespace moex
