@@ -47,6 +47,27 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// A place in a ring of N stages that K and V take in turn: the stage and the
+// parity of its current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+  __device__ __forceinline__ void next2() {
+    slot += 2;
+    if (slot >= N) {
+      slot -= N;
+      parity ^= 1;
+    }
+  }
+};
+
 // Shared-memory writes of this thread before reads by the tensor core.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int R>
@@ -56,6 +77,31 @@ __device__ __forceinline__ void regs_up() {
 template <int R>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// The larger of three, and FP32 arithmetic on pairs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 template <int CT, int D>
@@ -130,133 +176,164 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
   if (warp < 4) {
     // ------------------------------------------------ keys and values
     regs_down<80>();
-    const int c = threadIdx.x % CH, r0 = threadIdx.x / CH;  // chunk, row within a group of RPI rows
-    constexpr int RPI = 128 / CH;                            // rows a round of the 128 threads covers: 8 or 16
-    const uint32_t dst0 = (c >> 3) * L::HALF + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
-    int n = 0, told = 0;  // stages issued, stages announced
-    auto announce = [&](int upto) {
+    // A warp copies 32 keys of a block: four runs of 8, each inside one page.
+    constexpr int RPI = 32 / CH;      // rows an instruction covers: 2 or 4
+    constexpr int PER_RUN = 8 / RPI;  // instructions a run takes
+    const int c = lane % CH, r0 = lane / CH;
+    uint32_t dst0[PER_RUN];
+#pragma unroll
+    for (int i = 0; i < PER_RUN; ++i) {
+      const int r = i * RPI + r0;
+      dst0[i] = smb + L::RING + (c >> 3) * L::HALF + (32 * warp + r) * 128 + (((c & 7) ^ r) << 4);
+    }
+    const int64_t rows = RPI * a.b.row_stride, mine_at = r0 * a.b.row_stride + 8 * c;
+    Ring<NS> ring;
+    int told_slot = 0, untold = 0;  // stages under way that the MMA warp does not know of
+    bool filled = false;            // the ring has been filled once: stages have to be waited for
+    auto announce = [&](int keep) {
       fence_async_smem();
       __syncwarp();
-      for (; told < upto; ++told)
-        if (lane == 0) mbar_arrive(&kv_full[told % NS]);
+      for (; untold > keep; --untold) {
+        if (lane == 0) mbar_arrive(&kv_full[told_slot]);
+        told_slot = told_slot + 1 == NS ? 0 : told_slot + 1;
+      }
     };
     bool ok = true;
     while (cur.left > 0 && ok) {
       const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
       const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, b = cur.b, hk = cur.hk;
+      // lane l < 4: the page of this warp's run l of a block
+      auto fetch_page = [&](int j) {
+        j += 32 * warp + 8 * lane;
+        return lane < 4 && j < hi ? page_of(a.b, b, j) : -1;
+      };
+      int pg = fetch_page(first);
       for (int i = 0; i < units && ok; ++i) {
         const int j0 = first + i * UK;
-        // lane l < 16: the page of keys j0 + 8 l .. + 7
-        int pg = -1;
-        if (lane < 16 && j0 + 8 * lane < hi) pg = page_of(a.b, b, j0 + 8 * lane);
-        for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
-          const int slot = n % NS;
-          if (n >= NS && !__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[slot], ((n / NS) - 1) & 1))) {
+        // and the offset of its first row, -1 for none
+        const int64_t mine = pg < 0 ? -1 : kv_offset(a.b, pg, hk, j0 + 32 * warp + 8 * lane);
+        int64_t off[4];
+        bool whole = true;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          off[n] = __shfl_sync(0xffffffffu, mine, n);
+          whole = whole && off[n] >= 0;
+          off[n] += off[n] >= 0 ? mine_at : 0;
+        }
+        whole = whole && j0 + 32 * warp + 32 <= hi;
+        if (i + 1 < units) pg = fetch_page(j0 + UK);  // read a block ahead
+        for (int kv = 0; kv < 2; ++kv) {
+          if (filled && !__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[ring.slot], ring.parity ^ 1))) {
             // about to wait: hand over everything that is under way first
             cp_wait<0>();
-            announce(n);
-            ok = warp_wait(&kv_empty[slot], ((n / NS) - 1) & 1, DEV_TIMEOUT_PIPE);
+            announce(0);
+            ok = warp_wait(&kv_empty[ring.slot], ring.parity ^ 1, DEV_TIMEOUT_PIPE);
             if (!ok) break;
           }
-          const uint32_t dst = smb + L::RING + slot * L::STAGE + dst0;
-          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.v : a.k) + 8 * c;
-#pragma unroll 4
-          for (int it = 0; it < 128 / RPI; ++it) {
-            const int r = it * RPI + r0, j = j0 + r;
-            const int page = __shfl_sync(0xffffffffu, pg, r >> 3);
-            const bool in = j < hi && page >= 0;
-            cp_async16(dst + it * RPI * 128, src + (in ? kv_offset(a.b, page, hk, j) : 0), in ? 16u : 0u);
+          const uint32_t dst = ring.slot * L::STAGE;
+          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.v : a.k);
+          if (whole) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint16_t* p = src + off[n];
+#pragma unroll
+              for (int k = 0; k < PER_RUN; ++k, p += rows) cp_async16(dst + dst0[k] + n * 1024, p, 16u);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int k = 0; k < PER_RUN; ++k) {
+                const bool in = off[n] >= 0 && j0 + 32 * warp + 8 * n + k * RPI + r0 < hi;
+                cp_async16(dst + dst0[k] + n * 1024, src + (in ? off[n] + k * rows : 0), in ? 16u : 0u);
+              }
           }
           cp_commit();
-          if (n >= 2) {
+          ++untold;
+          ring.next();
+          filled = filled || ring.slot == 0;
+          if (untold > 2) {
             cp_wait<2>();
-            announce(n - 1);
+            announce(2);
           }
         }
       }
       advance(units);
     }
     cp_wait<0>();
-    if (ok) announce(n);
+    if (ok) announce(0);
   } else if (warp >= 12) {
     regs_down<80>();
     if (warp == 12) {
       // ------------------------------------------------ MMA issue
-      if (lane == 0) {
-        constexpr uint32_t IDESC_S = idesc_16_f32(128, 128, CT == MOEX_BF16, false);
-        constexpr uint32_t IDESC_O = idesc_16_f32(128, D, CT == MOEX_BF16, true);
-        const uint64_t qd = smem_desc_sw128(smb + L::Q);
-        const uint64_t kd = smem_desc_sw128(smb + L::RING);
-        const uint64_t vd = smem_desc_mn_sw128(smb + L::RING, L::HALF);
-        int n = 0, tile = 0;
-        int np[2] = {0, 0}, no[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, abort_flag)) {
-            if (!*abort_flag) flag_status(a.b.status, DEV_TIMEOUT_MMA);
-            *abort_flag = 1;
-            ok = false;
-          }
-          return ok;
-        };
-        auto first = [&](int g, int slot) {  // S_g = Q_g K^T
+      constexpr uint32_t IDESC_S = idesc_16_f32(128, 128, CT == MOEX_BF16, false);
+      constexpr uint32_t IDESC_O = idesc_16_f32(128, D, CT == MOEX_BF16, true);
+      const uint64_t qd = smem_desc_sw128(smb + L::Q);
+      const uint64_t kd = smem_desc_sw128(smb + L::RING);
+      const uint64_t vd = smem_desc_mn_sw128(smb + L::RING, L::HALF);
+      Ring<NS> kr, vr;  // the stages of the next keys and values
+      vr.next();
+      uint32_t qp = 0, pp[2] = {0, 0}, op[2] = {1, 1};  // parities; the first O finds its columns free
+      bool ok = true;
+      auto first = [&](int g, int slot) {  // S_g = Q_g K^T
+        const uint64_t kb = kd + slot * (L::STAGE >> 4), qb = qd + g * (L::STAGE >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4;
-            mma_f16_ss(tmem + g * 128, qd + ((g * L::STAGE) >> 4) + off, kd + ((slot * L::STAGE) >> 4) + off, IDESC_S,
-                       ks != 0);
-          }
-        };
-        auto second = [&](int g, int slot, bool acc) {  // O_g (+)= P_g V
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * ks, vd + ((slot * L::STAGE + ks * 2048) >> 4), IDESC_O,
-                       acc || ks != 0);
-        };
-        while (cur.left > 0 && ok) {
-          const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
-          const int groups = cur.x.r1 - cur.x.r0 > 128 ? 2 : 1;
-          if (!wait(q_full, tile & 1)) break;
-          if (!wait(&kv_full[n % NS], (n / NS) & 1)) break;
-          tc_fence_after();
-          for (int g = 0; g < groups; ++g) {
-            first(g, n % NS);
-            mma_commit(&s_full[g]);
-          }
-          mma_commit(&kv_empty[n % NS]);
-          if (units == 1) mma_commit(q_empty);
-          for (int i = 0; i < units && ok; ++i, n += 2) {
-            const int vs = (n + 1) % NS, ks = (n + 2) % NS;
-            if (!wait(&kv_full[vs], ((n + 1) / NS) & 1)) break;
-            for (int g = 0; g < groups && ok; ++g) {
-              if (i == 0 && no[g] > 0 && !wait(&o_empty[g], (no[g] - 1) & 1)) break;
-              if (!wait(&p_full[g], np[g] & 1)) break;
-              ++np[g];
-              tc_fence_after();
-              second(g, vs, i > 0);
-              if (g == groups - 1) mma_commit(&kv_empty[vs]);
-              if (i + 1 < units) {
-                if (g == 0 && !wait(&kv_full[ks], ((n + 2) / NS) & 1)) break;
-                tc_fence_after();
-                first(g, ks);
-                mma_commit(&s_full[g]);
-                if (g == groups - 1) {
-                  mma_commit(&kv_empty[ks]);
-                  if (i + 2 == units) mma_commit(q_empty);
-                }
-              } else {
-                mma_commit(&o_full[g]);
-                ++no[g];
-              }
-            }
-          }
-          ++tile;
-          next_tile<MT, UK>(a, cur, units);  // this lane alone
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4;
+          mma_f16_ss_elect(tmem + g * 128, qb + off, kb + off, IDESC_S, ks != 0);
         }
-        // the CTA leaves its TMEM and shared memory only when nothing reads them any more
-        mma_commit(done);
-        mbar_wait(done, 0, nullptr);
+        mma_commit_elect(&s_full[g]);
+      };
+      auto second = [&](int g, int slot, bool acc) {  // O_g (+)= P_g V
+        const uint64_t vb = vd + slot * (L::STAGE >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_f16_ts_elect(tmem + 256 + g * 128, tmem + g * 128 + 8 * ks, vb + ks * (2048 >> 4), IDESC_O, acc || ks != 0);
+      };
+      while (cur.left > 0 && ok) {
+        const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+        const int groups = cur.x.r1 - cur.x.r0 > 128 ? 2 : 1;
+        ok = warp_wait(q_full, qp, DEV_TIMEOUT_MMA) && warp_wait(&kv_full[kr.slot], kr.parity, DEV_TIMEOUT_MMA);
+        if (!ok) break;
+        qp ^= 1;
+        tc_fence_after();
+        first(0, kr.slot);
+        if (groups == 2) first(1, kr.slot);
+        mma_commit_elect(&kv_empty[kr.slot]);
+        if (units == 1) mma_commit_elect(q_empty);
+        for (int i = 0; i < units; ++i) {
+          const bool more = i + 1 < units;
+          kr.next2();
+          ok = warp_wait(&kv_full[vr.slot], vr.parity, DEV_TIMEOUT_MMA);
+          if (ok && more) ok = warp_wait(&kv_full[kr.slot], kr.parity, DEV_TIMEOUT_MMA);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (!ok || g >= groups) break;
+            if (i == 0) {
+              ok = warp_wait(&o_empty[g], op[g], DEV_TIMEOUT_MMA);
+              op[g] ^= 1;
+            }
+            ok = ok && warp_wait(&p_full[g], pp[g], DEV_TIMEOUT_MMA);
+            if (!ok) break;
+            pp[g] ^= 1;
+            tc_fence_after();
+            second(g, vr.slot, i > 0);
+            if (g == groups - 1) mma_commit_elect(&kv_empty[vr.slot]);
+            if (more)
+              first(g, kr.slot);
+            else
+              mma_commit_elect(&o_full[g]);
+          }
+          if (!ok) break;
+          if (more) mma_commit_elect(&kv_empty[kr.slot]);
+          if (i + 2 == units) mma_commit_elect(q_empty);
+          vr.next2();
+        }
+        advance(units);
       }
+      // the CTA leaves its TMEM and shared memory only when nothing reads them any more
+      mma_commit_elect(done);
+      mbar_wait(done, 0, nullptr);
       __syncwarp();
     } else {
       // ------------------------------------------------ queries
@@ -332,9 +409,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < 32; e += 2)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
           const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
           const bool grow = top_s > m + GROW || (i == 0 && top_s > m) || (m == -INFINITY && top_s > m);
           if (__any_sync(0xffffffffu, grow)) {
@@ -355,21 +432,27 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+          uint64_t sum[2] = {0, 0};  // pairs of FP32 sums
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(s[q][2 * e]), a.scale_log2, -ref));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(s[q][2 * e + 1]), a.scale_log2, -ref));
-              sum[e & 1] += p0;
-              sum[2 + (e & 1)] += p1;
+              float p0, p1;
+              unpack2(fma2(pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1])), scale2, ref2), p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
               pk[e] = E::pack(p0, p1);
             }
             tmem_st16(ts + 16 * q, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          {
+            float s0, s1;
+            unpack2(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
