@@ -30,9 +30,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = c0; c <= c1; ++c) {
       if (range_begin(c, x.W, n_cta) == range_begin(c + 1, x.W, n_cta)) continue;  // no units, no partial
-      const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * MT + r;
+      const int64_t slot = 2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0), at = slot * MT + r;
       const float2 p = *reinterpret_cast<const float2*>(ml + 2 * at);
-      const float4 v = *reinterpret_cast<const float4*>(a.part + at * D + c4);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + part_offset<MT, D>(slot, r, c4));
       const float mn = fmaxf(m, p.x), ref = mn == -INFINITY ? 0.f : mn;
       const float f0 = fast_exp2(m - ref), f1 = fast_exp2(p.x - ref);
       m = mn;

@@ -32,7 +32,7 @@ struct AttnArgs {
   void* out;
   float* lse;         // or nullptr
   struct RangeStart* plan;  // [G]
-  float* part;        // [2 G][MT][D], then [2 G][MT][2]
+  float* part;        // [2 G] tiles of MT x D (part_offset), then [2 G][MT][2]
   int64_t ldq, ldo;
   float scale_log2;   // scale * log2(e): scores are kept in powers of two
   int n_heads, n_kv_heads, group, window, out_f32;
@@ -66,11 +66,14 @@ __device__ __forceinline__ Tile tile_of(const SeqView& s, int group, int window,
   return x;
 }
 
+// Units of a sequence and key head, the warp's lanes taking tiles in turn.
 template <int MT, int UK>
-__device__ __forceinline__ int64_t seq_units(const SeqView& s, int group, int window) {
+__device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, int group, int window) {
   const int tiles = (s.n * group + MT - 1) / MT;
   int64_t u = 0;
-  for (int t = 0; t < tiles; ++t) u += tile_of<MT, UK>(s, group, window, t).units;
+  for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_of<MT, UK>(s, group, window, t).units;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   return u;
 }
 
@@ -92,7 +95,7 @@ struct Cursor {
 template <int MT, int UK, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
   __shared__ int64_t warp_sum[2][THREADS / 32];
-  __shared__ int64_t found[2];  // sequence, units before it
+  __shared__ int64_t found[3];  // sequence, units before it, its units
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total = 0, mine = 0, before = 0;
   // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
@@ -102,12 +105,18 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
     for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
       const int b = base + threadIdx.x;
       if (pass == 0 || a.b.n_seqs > THREADS) {
-        int64_t v = 0;
-        if (b < a.b.n_seqs) {
-          const SeqView s = seq_view(a.b, b);
-          if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-          v = s.n > 0 ? a.n_kv_heads * seq_units<MT, UK>(s, a.group, a.window) : 0;
+        // a thread a sequence; one of several tiles is counted by the whole warp
+        SeqView s{0, 0, 0, false};
+        if (b < a.b.n_seqs) s = seq_view(a.b, b);
+        if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+        int64_t v = s.n > 0 ? tile_of<MT, UK>(s, a.group, a.window, 0).units : 0;
+        for (uint32_t many = __ballot_sync(0xffffffffu, s.n * a.group > MT); many; many &= many - 1) {
+          const int src = __ffs(many) - 1;
+          SeqView w{0, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.ctx, src), false};
+          const int64_t u = seq_units_warp<MT, UK>(w, a.group, a.window);
+          if (lane == src) v = u;
         }
+        v *= a.n_kv_heads;
         mine = v;
         int64_t x = v;
 #pragma unroll
@@ -128,6 +137,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
       if (pass == 1 && mine > 0 && before <= want && want < before + mine) {
         found[0] = b;
         found[1] = before;
+        found[2] = mine;
       }
     }
     if (pass == 0) total = run;
@@ -142,14 +152,29 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   cur.b = static_cast<int>(found[0]);
   cur.s = seq_view(a.b, cur.b);
   int64_t off = u0 - found[1];
-  const int64_t per = seq_units<MT, UK>(cur.s, a.group, a.window);
+  const int64_t per = found[2] / a.n_kv_heads;
   cur.hk = static_cast<int>(off / per);
   off -= cur.hk * per;
-  for (cur.t = 0;; ++cur.t) {
-    cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
-    if (off < cur.x.units) break;
-    off -= cur.x.units;
+  // the tile: 32 at a time, every warp for itself
+  for (int t0 = 0;; t0 += 32) {
+    const int t = t0 + lane;
+    int n = t * MT < cur.s.n * a.group ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units : 0;
+    int64_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, sum > off);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      cur.t = t0 + src;
+      off -= __shfl_sync(0xffffffffu, sum - n, src);
+      break;
+    }
+    off -= __shfl_sync(0xffffffffu, sum, 31);
   }
+  cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
   cur.u = static_cast<int>(off);
   if (threadIdx.x == 0)
     a.plan[cta] = RangeStart{total, u0 - off, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0};
@@ -178,6 +203,15 @@ __device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int do
 __device__ __forceinline__ int64_t row_offset(const SeqView& s, int group, int hk, int r, int64_t ld, int D) {
   const int i = r / group;
   return (s.first + i) * ld + static_cast<int64_t>(hk * group + (r - i * group)) * D;
+}
+
+// Float offset of columns c .. c + 3 (c a multiple of 4) of a row of partial
+// tile `slot`: 32 rows' pieces lie side by side, as a warp of one row a lane
+// writes them.
+template <int MT, int D>
+__device__ __forceinline__ int64_t part_offset(int64_t slot, int row, int c) {
+  constexpr int R = MT < 32 ? MT : 32;
+  return (slot * MT + row / R * R) * D + (c / 4 * R + row % R) * 4;
 }
 
 template <int CT>

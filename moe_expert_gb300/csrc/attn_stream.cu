@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
           a.lse[row_offset(cur.s, a.group, cur.hk, x.r0 + r, a.n_heads, 1)] =
               ll > 0.f ? mm * LN2 + logf(ll) : -INFINITY;
       } else {
-        *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * MT + r) * D + c) = acc;
+        *reinterpret_cast<float4*>(a.part + part_offset<MT, D>(slot, r, c)) = acc;
         if (c == 0) {
           float* ml = a.part + static_cast<int64_t>(2 * gridDim.x) * MT * D + (static_cast<int64_t>(slot) * MT + r) * 2;
           ml[0] = mm;

@@ -47,6 +47,17 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Whether the phase is complete, at once (try_wait may suspend the thread first).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A place in a ring of N stages that K and V take in turn: the stage and the
 // parity of its current use.
 template <int N>
@@ -102,6 +113,56 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// Writes 64 bytes of each lane's row (16 FP32 values, or 32 rounded to 16 bits):
+// the 4 x 4 sixteen-byte pieces of four lanes are exchanged, so that four lanes
+// write 64 bytes of one row and a store touches 8 rows, not 32.  off: the row's
+// element offset, -1 for none.
+template <int TYPE>
+__device__ __forceinline__ void store_rows(void* out, int64_t off, int col, const uint32_t* v, int lane) {
+  uint32_t w[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (TYPE == MOEX_F32)
+        w[i][j] = v[4 * i + j];
+      else
+        w[i][j] = RowElem<TYPE>::pack(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+    }
+  // transpose over the lane's two low bits: piece i of lane k <-> piece k of lane i
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & b)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool up = lane & b;
+          const uint32_t send = up ? w[i][j] : w[i | b][j];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, send, b);
+          if (up)
+            w[i][j] = got;
+          else
+            w[i | b][j] = got;
+        }
+      }
+  constexpr int PIECE = TYPE == MOEX_F32 ? 4 : 8;  // elements of 16 bytes
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t o = __shfl_sync(0xffffffffu, off, (lane & ~3) | i);  // the row of lane 4 * (lane / 4) + i
+    if (o >= 0) {
+      void* p = TYPE == MOEX_F32 ? static_cast<void*>(static_cast<float*>(out) + o + col + PIECE * (lane & 3))
+                                 : static_cast<void*>(static_cast<uint16_t*>(out) + o + col + PIECE * (lane & 3));
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+    }
+  }
+}
+
+// A word with its n lowest bits set (none below 0, all above 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 template <int CT, int D>
@@ -201,17 +262,23 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
     bool ok = true;
     while (cur.left > 0 && ok) {
       const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
-      const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, b = cur.b, hk = cur.hk;
-      // lane l < 4: the page of this warp's run l of a block
+      const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, hk = cur.hk;
+      const int32_t* table = a.b.table + cur.b * a.b.table_stride;
+      // lane l < 4: the page of this warp's run l of a block, read a block ahead and looked at when its turn comes
       auto fetch_page = [&](int j) {
         j += 32 * warp + 8 * lane;
-        return lane < 4 && j < hi ? page_of(a.b, b, j) : -1;
+        return lane < 4 && j < hi ? __ldg(table + (j >> a.b.page_shift)) : -1;
       };
       int pg = fetch_page(first);
       for (int i = 0; i < units && ok; ++i) {
-        const int j0 = first + i * UK;
-        // and the offset of its first row, -1 for none
-        const int64_t mine = pg < 0 ? -1 : kv_offset(a.b, pg, hk, j0 + 32 * warp + 8 * lane);
+        const int j0 = first + i * UK, j = j0 + 32 * warp + 8 * lane;
+        // the offset of the run's first row, -1 for none
+        int64_t mine = -1;
+        if (pg >= 0 && pg < a.b.n_pages)
+          mine = kv_offset(a.b, pg, hk, j);
+        else if (lane < 4 && j < hi)
+          flag_status(a.b.status, DEV_BAD_BATCH);
+        if (i + 1 < units) pg = fetch_page(j0 + UK);
         int64_t off[4];
         bool whole = true;
 #pragma unroll
@@ -221,9 +288,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           off[n] += off[n] >= 0 ? mine_at : 0;
         }
         whole = whole && j0 + 32 * warp + 32 <= hi;
-        if (i + 1 < units) pg = fetch_page(j0 + UK);  // read a block ahead
         for (int kv = 0; kv < 2; ++kv) {
-          if (filled && !__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[ring.slot], ring.parity ^ 1))) {
+          if (filled && !__all_sync(0xffffffffu, mbar_test(&kv_empty[ring.slot], ring.parity ^ 1))) {
             // about to wait: hand over everything that is under way first
             cp_wait<0>();
             announce(0);
@@ -341,15 +407,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
       while (cur.left > 0) {
         const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
         if (tile > 0 && !warp_wait(q_empty, (tile - 1) & 1, DEV_TIMEOUT_PIPE)) break;
-        const int rows = cur.x.r1 - cur.x.r0;
-#pragma unroll 2
-        for (int i = threadIdx.x - 13 * 32; i < (rows > 128 ? 256 : 128) * CH; i += 96) {
-          const int r = i / CH, c = i % CH;
-          const bool in = r < rows;
-          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
-                                (in ? row_offset(cur.s, a.group, cur.hk, cur.x.r0 + r, a.ldq, D) + 8 * c : 0);
-          cp_async16(smb + L::Q + (r >> 7) * L::STAGE + (c >> 3) * L::HALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     src, in ? 16u : 0u);
+        // 32 rows at a time: lane l finds where row l is, then the warp copies RPI rows an instruction
+        constexpr int RPI = 32 / CH;
+        const int rows = cur.x.r1 - cur.x.r0, c = lane % CH;
+        for (int r0 = 32 * (warp - 13); r0 < rows; r0 += 96) {
+          const int64_t mine = r0 + lane < rows ? row_offset(cur.s, a.group, cur.hk, cur.x.r0 + r0 + lane, a.ldq, D) : -1;
+          const uint32_t dst = smb + L::Q + (r0 >> 7) * L::STAGE + (c >> 3) * L::HALF + (r0 & 127) * 128;
+#pragma unroll 8
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int r = i * RPI + lane / CH;
+            const int64_t off = __shfl_sync(0xffffffffu, mine, r);
+            cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                       static_cast<const uint16_t*>(a.q) + (off >= 0 ? off + 8 * c : 0), off >= 0 ? 16u : 0u);
+          }
         }
         cp_commit();
         cp_wait<0>();
@@ -379,15 +449,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
         const int top = in ? cur.s.ctx - cur.s.n + r / a.group : -1;
         const int bot = a.window > 0 ? top - a.window : -1;
         float m = -INFINITY, l = 0.f;
+        // lane c < 16: the page of keys j + 8 c .. + 7 of a block, read a block ahead (0 where there is no such key)
+        auto fetch_page = [&](int j) {
+          j += 8 * lane;
+          return lane < 16 && j < end ? __ldg(table + (j >> a.b.page_shift)) : 0;
+        };
+        int pg = fetch_page(first);
         for (int i = 0; i < units; ++i, ++ns) {
           const int j0 = first + i * UK;
-          // keys without a page (lane c: keys j0 + 8 c .. + 7); read while the product runs
-          int pg = 0;
-          if (lane < 16 && j0 + 8 * lane < end) {
-            pg = table[(j0 + 8 * lane) >> a.b.page_shift];
-            pg = pg < 0 || pg >= a.b.n_pages;
-          }
-          const uint32_t bad = __ballot_sync(0xffffffffu, pg != 0);
+          // runs of eight keys without a page
+          const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.b.n_pages);
+          if (i + 1 < units) pg = fetch_page(j0 + UK);
           ok = warp_wait(&s_full[g], ns & 1, DEV_TIMEOUT_MMA);
           if (!ok) break;
           tc_fence_after();
@@ -398,14 +470,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           // every key of the block seen by every row of the warp?
           const bool clean = __all_sync(0xffffffffu, j0 + UK - 1 <= top && j0 > bot) && bad == 0;
           if (!clean) {
-            const int hi = top - j0, lo = bot - j0;
+            const int hi = top - j0, lo = bot - j0;  // keys lo < c <= hi of the block are seen
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {
+              // one bit a key
+              uint32_t seen = low_bits(hi + 1 - 32 * q) & ~low_bits(lo + 1 - 32 * q);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int c = 32 * q + e;
-                if (!(c <= hi && c > lo) || ((bad >> (c >> 3)) & 1u)) s[q][e] = 0xff800000u;  // -inf
-              }
+              for (int k = 0; k < 4; ++k)
+                if ((bad >> (4 * q + k)) & 1u) seen &= ~(0xFFu << (8 * k));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((seen >> e) & 1u)) s[q][e] = 0xff800000u;  // -inf
+            }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -467,8 +543,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
         const bool whole = units == cur.x.units;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u == 0 ? 1 : 0);
         const float inv = whole ? (l > 0.f ? __fdiv_rn(1.f, l) : 0.f) : 1.f;
-        const int64_t off = in ? row_offset(cur.s, a.group, cur.hk, r, a.ldo, D) : 0;
-        float* part = a.part + (slot * MT + row) * D;
+        const int64_t off = in ? row_offset(cur.s, a.group, cur.hk, r, a.ldo, D) : -1;
+        float* part = a.part + part_offset<MT, D>(slot, row, 0);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -479,26 +555,26 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty[g]);
           }
-          if (in) {
+          if (!whole) {
+            // lanes side by side: a warp's store is 512 bytes in a row
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float v[8];
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + (8 * q + e / 4) * 128) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
 #pragma unroll
-              for (int w = 0; w < 8; ++w) v[w] = __uint_as_float(o[e + w]) * inv;
-              if (!whole)
-                store8<MOEX_F32>(part, 32 * q + e, v);
-              else if (a.out_f32)
-                store8<MOEX_F32>(a.out, off + 32 * q + e, v);
-              else
-                store8<CT>(a.out, off + 32 * q + e, v);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+            if (a.out_f32) {
+              store_rows<MOEX_F32>(a.out, off, 32 * q, o, lane);
+              store_rows<MOEX_F32>(a.out, off, 32 * q + 16, o + 16, lane);
+            } else {
+              store_rows<CT>(a.out, off, 32 * q, o, lane);
             }
           }
         }
         if (in) {
           if (!whole) {
-            float* ml = a.part + 2 * static_cast<int64_t>(gridDim.x) * MT * D + (slot * MT + row) * 2;
-            ml[0] = m;
-            ml[1] = l;
+            *reinterpret_cast<float2*>(a.part + 2 * static_cast<int64_t>(gridDim.x) * MT * D + (slot * MT + row) * 2) =
+                make_float2(m, l);
           } else if (a.lse) {
             a.lse[row_offset(cur.s, a.group, cur.hk, r, a.n_heads, 1)] =
                 l > 0.f ? m * LN2 + logf(l) : -INFINITY;
