@@ -7,44 +7,97 @@
 namespace moex {
 
 // Tiles that ranges cut, one column of CTAs for each range that begins inside a
-// tile and is the first to do so: the partials in the order of their keys, FP32.
-// CTA c leaves its first tile in slot 2c when it begins inside it, and its last
-// in slot 2c + 1 when it does not finish it.
+// tile and is the first to do so, a CTA for 32 rows: the partials in the order of
+// their keys, FP32.  CTA c of the first kernel leaves its first tile in slot 2c
+// when it begins inside it, and its last in slot 2c + 1 when it does not finish
+// it.  Latency bounds this kernel, so the rows' weights of up to 32 partials are
+// formed first and the partials then read independently of one another.
 template <int CT, int D, int MT>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a) {
-  const int n_cta = gridDim.x;
+  constexpr int R = MT < 32 ? MT : 32, F = 32, V = D / 4, ITEMS = R * V / 128;
+  __shared__ float2 ml[F][R];          // (maximum, sum), then (weight, sum)
+  __shared__ float rescale[R], total[R], top[R];
+  __shared__ float4 rows[R][V + 1];
+  const int n_cta = gridDim.x, r0 = blockIdx.y * R;
   pdl_wait();
   pdl_launch_dependents();
   const RangeStart x = a.plan[blockIdx.x];
-  if (x.u == 0) return;  // begins with a tile, or has no units
+  if (x.u == 0 || r0 >= x.rows) return;  // begins with a tile, or has no units
   const int64_t u0 = x.tile_u + x.u;
-  const int c0 = static_cast<int>(range_of(x.tile_u, x.W, n_cta));
   if (range_begin(range_of(u0 - 1, x.W, n_cta), x.W, n_cta) > x.tile_u) return;  // an earlier range cut it first
-  const int c1 = static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta));
-  const SeqView s = seq_view(a.b, x.b);
-  const float* ml = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
-  constexpr int V = D / 4;
-  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < x.rows * V; i += gridDim.y * blockDim.x) {
-    const int r = i / V, c4 = 4 * (i % V);
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      if (range_begin(c, x.W, n_cta) == range_begin(c + 1, x.W, n_cta)) continue;  // no units, no partial
-      const int64_t slot = 2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0), at = slot * MT + r;
-      const float2 p = *reinterpret_cast<const float2*>(ml + 2 * at);
-      const float4 v = *reinterpret_cast<const float4*>(a.part + part_offset<MT, D>(slot, r, c4));
-      const float mn = fmaxf(m, p.x), ref = mn == -INFINITY ? 0.f : mn;
-      const float f0 = fast_exp2(m - ref), f1 = fast_exp2(p.x - ref);
-      m = mn;
-      l = l * f0 + p.y * f1;
-      acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
-      acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+  const int c0 = static_cast<int>(range_of(x.tile_u, x.W, n_cta));
+  // with fewer units than CTAs a range is one unit or none
+  const bool sparse = x.W < n_cta;
+  const int parts = sparse ? x.units : static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta)) - c0 + 1;
+  auto slot_of = [&](int f) -> int64_t {
+    const int64_t c = sparse ? range_of(x.tile_u + f, x.W, n_cta) : c0 + f;
+    return 2 * c + (f == 0 ? 1 : 0);
+  };
+  const int nr = min(R, x.rows - r0);
+  const float* stats = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
+  float4 acc[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int f0 = 0; f0 < parts; f0 += F) {
+    const int nf = min(F, parts - f0);
+    for (int i = threadIdx.x; i < nf * R; i += 128)
+      if (i % R < nr)
+        ml[i / R][i % R] = *reinterpret_cast<const float2*>(stats + 2 * (slot_of(f0 + i / R) * MT + r0 + i % R));
+    __syncthreads();
+    if (threadIdx.x < nr) {
+      const int r = threadIdx.x;
+      const float old = f0 ? top[r] : -INFINITY;
+      float m = old, l = 0.f;
+      for (int f = 0; f < nf; ++f) m = fmaxf(m, ml[f][r].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      for (int f = 0; f < nf; ++f) {
+        const float w = fast_exp2(ml[f][r].x - ref);
+        l += w * ml[f][r].y;
+        ml[f][r].x = w;
+      }
+      const float k = fast_exp2(old - ref);
+      rescale[r] = k;
+      total[r] = (f0 ? total[r] * k : 0.f) + l;
+      top[r] = m;
     }
-    const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
-    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-    store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r, a.ldo, D) + c4, acc);
-    if (a.lse && c4 == 0)
-      a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int r = (threadIdx.x + 128 * k) % R;
+      const float old = r < nr ? rescale[r] : 0.f;
+      acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
+    }
+#pragma unroll 4
+    for (int f = 0; f < nf; ++f) {
+      const float* part = a.part + part_offset<MT, D>(slot_of(f0 + f), r0, 0);
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        const int i = threadIdx.x + 128 * k;  // columns 4 (i / R) of row i % R
+        if (i % R < nr) {
+          const float4 v = *reinterpret_cast<const float4*>(part + 4 * i);
+          const float w = ml[f][i % R].x;
+          acc[k].x += w * v.x, acc[k].y += w * v.y, acc[k].z += w * v.z, acc[k].w += w * v.w;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // by way of shared memory, so that a row is written in one piece
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int i = threadIdx.x + 128 * k;
+    rows[i % R][i / R] = acc[k];
+  }
+  __syncthreads();
+  const SeqView s = seq_view(a.b, x.b);
+  for (int i = threadIdx.x; i < nr * V; i += 128) {
+    const int r = i / V, row = x.t * MT + r0 + r;
+    const float l = total[r], inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+    float4 v = rows[r][i % V];
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    store_out4<CT>(a, row_offset(s, a.group, x.hk, row, a.ldo, D) + 4 * (i % V), v);
+    if (a.lse && i % V == 0)
+      a.lse[row_offset(s, a.group, x.hk, row, a.n_heads, 1)] = l > 0.f ? top[r] * LN2 + logf(l) : -INFINITY;
   }
 }
 
@@ -69,7 +122,7 @@ AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads) {
 
 template <int CT, int D>
 cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
-  if (g.tile) return launch_pdl(attend_join_kernel<CT, D, TILE_MT>, dim3(g.ctas, 8), dim3(128), 0, s, a);
+  if (g.tile) return launch_pdl(attend_join_kernel<CT, D, TILE_MT>, dim3(g.ctas, TILE_MT / 32), dim3(128), 0, s, a);
   return launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, dim3(g.ctas), dim3(128), 0, s, a);
 }
 

@@ -77,9 +77,16 @@ __device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, int group, i
   return u;
 }
 
-__host__ __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t W, int64_t G) { return c * W / G; }
+// (32-bit division where the numbers allow it: there are at most a few hundred CTAs.)
+__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t W, int G) {
+  const int64_t n = c * W;
+  return n >> 32 ? n / G : static_cast<uint32_t>(n) / static_cast<uint32_t>(G);
+}
 // The CTA whose range holds unit u.
-__host__ __device__ __forceinline__ int64_t range_of(int64_t u, int64_t W, int64_t G) { return ((u + 1) * G - 1) / W; }
+__device__ __forceinline__ int64_t range_of(int64_t u, int64_t W, int G) {
+  const int64_t n = (u + 1) * G - 1;
+  return (n | W) >> 32 ? n / W : static_cast<uint32_t>(n) / static_cast<uint32_t>(W);
+}
 
 // Where a CTA is in the list of units.
 struct Cursor {
@@ -95,9 +102,12 @@ struct Cursor {
 template <int MT, int UK, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
   __shared__ int64_t warp_sum[2][THREADS / 32];
-  __shared__ int64_t found[3];  // sequence, units before it, its units
+  __shared__ int64_t found[2];  // units before the sequence, its units
+  __shared__ SeqView found_s;
+  __shared__ int found_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total = 0, mine = 0, before = 0;
+  SeqView s{0, 0, 0, false};
   // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
   for (int pass = 0; pass < 2; ++pass) {
     const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
@@ -106,7 +116,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
       const int b = base + threadIdx.x;
       if (pass == 0 || a.b.n_seqs > THREADS) {
         // a thread a sequence; one of several tiles is counted by the whole warp
-        SeqView s{0, 0, 0, false};
+        s = SeqView{0, 0, 0, false};
         if (b < a.b.n_seqs) s = seq_view(a.b, b);
         if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
         int64_t v = s.n > 0 ? tile_of<MT, UK>(s, a.group, a.window, 0).units : 0;
@@ -118,16 +128,20 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         }
         v *= a.n_kv_heads;
         mine = v;
+        // sums over the warps that have sequences
+        const int warps = min((a.b.n_seqs - base + 31) / 32, THREADS / 32);
         int64_t x = v;
+        if (warp < warps) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          if (lane == 31) warp_sum[it & 1][warp] = x;
         }
-        if (lane == 31) warp_sum[it & 1][warp] = x;
         __syncthreads();
         before = run;
-        for (int w = 0; w < THREADS / 32; ++w) {
+        for (int w = 0; w < warps; ++w) {
           const int64_t ws = warp_sum[it & 1][w];
           if (w < warp) before += ws;
           run += ws;
@@ -135,13 +149,16 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         before += x - v;
       }
       if (pass == 1 && mine > 0 && before <= want && want < before + mine) {
-        found[0] = b;
-        found[1] = before;
-        found[2] = mine;
+        found_b = b;
+        found_s = s;
+        found[0] = before;
+        found[1] = mine;
       }
     }
-    if (pass == 0) total = run;
-    __syncthreads();
+    if (pass == 0)
+      total = run;
+    else
+      __syncthreads();
   }
   const int64_t u0 = range_begin(cta, total, n_cta);
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
@@ -149,11 +166,12 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
     if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
-  cur.b = static_cast<int>(found[0]);
-  cur.s = seq_view(a.b, cur.b);
-  int64_t off = u0 - found[1];
-  const int64_t per = found[2] / a.n_kv_heads;
-  cur.hk = static_cast<int>(off / per);
+  cur.b = found_b;
+  cur.s = found_s;
+  int64_t off = u0 - found[0];
+  const int64_t per = found[1] >> 32 ? found[1] / a.n_kv_heads
+                                     : static_cast<uint32_t>(found[1]) / static_cast<uint32_t>(a.n_kv_heads);
+  cur.hk = static_cast<int>((off | per) >> 32 ? off / per : static_cast<uint32_t>(off) / static_cast<uint32_t>(per));
   off -= cur.hk * per;
   // the tile: 32 at a time, every warp for itself
   for (int t0 = 0;; t0 += 32) {
