@@ -120,6 +120,12 @@ AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads) {
   return g;
 }
 
+HeadGroup head_group(int n, int n_tokens) {
+  const int64_t rows = static_cast<int64_t>(n) * n_tokens + TILE_MT;  // a tile's row indices may pass the last row
+  const bool fits = n > 1 && rows * n < (int64_t(1) << 32);
+  return {n, fits ? static_cast<uint32_t>(((int64_t(1) << 32) + n - 1) / n) : 0u};
+}
+
 template <int CT, int D>
 cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
   if (g.tile) return launch_pdl(attend_join_kernel<CT, D, TILE_MT>, dim3(g.ctas, TILE_MT / 32), dim3(128), 0, s, a);
@@ -151,9 +157,9 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                    scale * 1.4426950408889634f,
                    n_heads,
                    kv->n_kv_heads,
-                   n_heads / kv->n_kv_heads,
                    window,
-                   out_type == MOEX_F32};
+                   out_type == MOEX_F32,
+                   head_group(n_heads / kv->n_kv_heads, batch->n_tokens)};
   const cudaError_t e = g.tile ? launch_attend_tile(a, kv->type, kv->head_dim, g.ctas, s)
                                : launch_attend_stream(a, kv->type, kv->head_dim, g.ctas, s);
   if (e != cudaSuccess) return MOEX_ECUDA;

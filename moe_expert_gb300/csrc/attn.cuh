@@ -17,6 +17,18 @@
 
 namespace moex {
 
+// Query heads of a key head, and division of a row index by it: r / n is the
+// high word of r * ceil(2^32 / n) as long as r * n < 2^32 (the product is above
+// r 2^32 / n by less than r < 2^32 / n); magic 0 where rows may be more.
+struct HeadGroup {
+  int n;
+  uint32_t magic;
+  __device__ __forceinline__ int token(int row) const {
+    if (n == 1) return row;
+    return magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), magic)) : row / n;
+  }
+};
+
 // Where a CTA's range begins, for the kernel that joins the tiles cut there.
 struct RangeStart {
   int64_t W, tile_u;     // units of the batch; units before the tile
@@ -35,7 +47,8 @@ struct AttnArgs {
   float* part;        // [2 G] tiles of MT x D (part_offset), then [2 G][MT][2]
   int64_t ldq, ldo;
   float scale_log2;   // scale * log2(e): scores are kept in powers of two
-  int n_heads, n_kv_heads, group, window, out_f32;
+  int n_heads, n_kv_heads, window, out_f32;
+  HeadGroup group;
 };
 
 constexpr float LN2 = 0.6931471805599453f;
@@ -54,13 +67,13 @@ struct Tile {
 };
 
 template <int MT, int UK>
-__device__ __forceinline__ Tile tile_of(const SeqView& s, int group, int window, int t) {
+__device__ __forceinline__ Tile tile_of(const SeqView& s, const HeadGroup& group, int window, int t) {
   Tile x;
   x.r0 = t * MT;
-  x.r1 = min(s.n * group, x.r0 + MT);
+  x.r1 = min(s.n * group.n, x.r0 + MT);
   const int base = s.ctx - s.n;
-  x.hi = max(base + (x.r1 - 1) / group + 1, 0);
-  x.lo = window > 0 ? max(base + x.r0 / group - window + 1, 0) & ~15 : 0;
+  x.hi = max(base + group.token(x.r1 - 1) + 1, 0);
+  x.lo = window > 0 ? max(base + group.token(x.r0) - window + 1, 0) & ~15 : 0;
   x.lo = min(x.lo, x.hi & ~15);
   x.units = max((x.hi - x.lo + UK - 1) / UK, 1);
   return x;
@@ -68,8 +81,8 @@ __device__ __forceinline__ Tile tile_of(const SeqView& s, int group, int window,
 
 // Units of a sequence and key head, the warp's lanes taking tiles in turn.
 template <int MT, int UK>
-__device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, int group, int window) {
-  const int tiles = (s.n * group + MT - 1) / MT;
+__device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, const HeadGroup& group, int window) {
+  const int tiles = (s.n * group.n + MT - 1) / MT;
   int64_t u = 0;
   for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_of<MT, UK>(s, group, window, t).units;
 #pragma unroll
@@ -120,7 +133,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         if (b < a.b.n_seqs) s = seq_view(a.b, b);
         if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
         int64_t v = s.n > 0 ? tile_of<MT, UK>(s, a.group, a.window, 0).units : 0;
-        for (uint32_t many = __ballot_sync(0xffffffffu, s.n * a.group > MT); many; many &= many - 1) {
+        for (uint32_t many = __ballot_sync(0xffffffffu, s.n * a.group.n > MT); many; many &= many - 1) {
           const int src = __ffs(many) - 1;
           SeqView w{0, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.ctx, src), false};
           const int64_t u = seq_units_warp<MT, UK>(w, a.group, a.window);
@@ -173,10 +186,11 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
                                      : static_cast<uint32_t>(found[1]) / static_cast<uint32_t>(a.n_kv_heads);
   cur.hk = static_cast<int>((off | per) >> 32 ? off / per : static_cast<uint32_t>(off) / static_cast<uint32_t>(per));
   off -= cur.hk * per;
+  cur.t = 0;
   // the tile: 32 at a time, every warp for itself
-  for (int t0 = 0;; t0 += 32) {
+  for (int t0 = 0; cur.s.n * a.group.n > MT; t0 += 32) {
     const int t = t0 + lane;
-    int n = t * MT < cur.s.n * a.group ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units : 0;
+    int n = t * MT < cur.s.n * a.group.n ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units : 0;
     int64_t sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -205,7 +219,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int do
   cur.u = 0;
   if (cur.left <= 0) return;
   ++cur.t;
-  if (cur.t * MT >= cur.s.n * a.group) {
+  if (cur.t * MT >= cur.s.n * a.group.n) {
     cur.t = 0;
     if (++cur.hk == a.n_kv_heads) {
       cur.hk = 0;
@@ -218,9 +232,9 @@ __device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int do
 }
 
 // Offset of row r of a tile's sequence and key head in a packed [token][head][D] buffer.
-__device__ __forceinline__ int64_t row_offset(const SeqView& s, int group, int hk, int r, int64_t ld, int D) {
-  const int i = r / group;
-  return (s.first + i) * ld + static_cast<int64_t>(hk * group + (r - i * group)) * D;
+__device__ __forceinline__ int64_t row_offset(const SeqView& s, const HeadGroup& group, int hk, int r, int64_t ld, int D) {
+  const int i = group.token(r);
+  return (s.first + i) * ld + static_cast<int64_t>(hk * group.n + (r - i * group.n)) * D;
 }
 
 // Float offset of columns c .. c + 3 (c a multiple of 4) of a row of partial

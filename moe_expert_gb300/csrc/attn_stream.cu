@@ -2,12 +2,12 @@
 // is streamed once, so DRAM bounds it.
 //
 // A CTA of four warps works on one tile of 16 rows; each warp runs alone
-// over every fourth step of 16 keys, with its own ring of copies in flight
-// (cp.async, no CTA barrier in the loop), its own running maximum and sum, and
-// the products on mma.sync m16n8k16: with 16 rows a step of 16 keys is 8 KB of
-// cache and 32 such instructions, far below the tensor rate, and tcgen05's
-// 128-row tiles would be mostly empty.  The four warps' results meet in shared
-// memory at the end of a tile.
+// over every fourth step of 16 keys, with its own copies in flight (cp.async,
+// no CTA barrier in the loop), its own running maximum and sum, and the
+// products on mma.sync m16n8k16: with 16 rows a step of 16 keys is 8 KB of cache
+// and 32 such instructions, far below the tensor rate, and tcgen05's 128-row
+// tiles would be mostly empty.  The copies run on from one tile into the next;
+// the four warps' results meet in shared memory at the end of a tile.
 #include "attn.cuh"
 #include "attn_launch.h"
 #include "internal.h"
@@ -16,7 +16,7 @@ namespace moex {
 namespace {
 
 constexpr int MT = STREAM_MT, UK = STREAM_UK;
-constexpr int WARPS = 4, STEP = 16, STAGES = 3;
+constexpr int WARPS = 4, STEP = 16, STAGES = 2;
 static_assert(UK == WARPS * STEP, "a unit is one step of every warp");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -53,15 +53,27 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Shared memory: the rings (warp, stage, K then V), reused at the end of a
-// tile for the warps' outputs [WARPS][MT][D + 4] and their maxima and sums.
+// Shared memory: each warp's two stages (K then V), and the warps' outputs
+// [WARPS][MT][D + 4] with their maxima and sums at the end of a tile.
 template <int D>
 struct Smem {
   static constexpr int PLANE = STEP * D * 2;   // bytes of a step's keys
   static constexpr int RING = WARPS * STAGES * 2 * PLANE;
   static constexpr int PITCH = D + 4;          // floats of an output row
-  static constexpr int JOIN = WARPS * MT * (PITCH + 2) * 4;
-  static constexpr int BYTES = RING > JOIN ? RING : JOIN;
+  static constexpr int BYTES = RING + WARPS * MT * (PITCH + 2) * 4;
+};
+
+// The keys of a tile that a CTA's range holds, as one warp sees them: steps
+// k0 + i * UK .. + 15.
+struct WarpKeys {
+  int units, k0, end, steps;
+  __device__ __forceinline__ WarpKeys(const Cursor& c, int warp) {
+    units = static_cast<int>(min(c.left, static_cast<int64_t>(c.x.units - c.u)));
+    const int first = c.x.lo + c.u * UK;
+    end = min(c.x.hi, first + units * UK);
+    k0 = first + warp * STEP;
+    steps = end > k0 ? (end - k0 + UK - 1) / UK : 0;
+  }
 };
 
 template <int CT, int D>
@@ -74,26 +86,88 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, p2 = 2 * (lane & 3);
   pdl_wait();
+  pdl_launch_dependents();  // the joining kernel's CTAs fit beside these, and wait
   Cursor cur;
   find_range<MT, UK, WARPS * 32>(a, blockIdx.x, gridDim.x, cur);
+  if (cur.left <= 0) return;
   const uint32_t ring = smem_u32(sm) + warp * STAGES * 2 * S::PLANE;
 
-  while (cur.left > 0) {
-    const Tile x = cur.x;
-    const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(x.units - cur.u)));
-    const int first = x.lo + cur.u * UK;  // this CTA's keys of the tile
-    const int end = min(x.hi, first + units * UK);
-    const int base = cur.s.ctx - cur.s.n;
+  // ---- copies: a cursor of their own, a step ahead of the products
+  __shared__ Cursor ahead_of[WARPS];
+  Cursor& ahead = ahead_of[warp];
+  if (lane == 0) ahead = cur;
+  __syncwarp();
+  int l_i = 0, l_steps = 0, l_k0 = 0, l_end = 0, l_hk = 0;  // the tile that copies are issued for
+  bool l_more = true;
+  int pg0 = -1, pg1 = -1;  // lane l: pages of step 32 * (l_i / 32) + l, its first and second eight keys
+  const int32_t* l_table = nullptr;
+  auto fetch_pages = [&]() {
+    const int j = l_k0 + (l_i + lane) * UK;
+    pg0 = j < l_end ? __ldg(l_table + (j >> a.b.page_shift)) : -1;
+    pg1 = j + 8 < l_end ? __ldg(l_table + ((j + 8) >> a.b.page_shift)) : pg0;
+  };
+  // the next tile in which this warp has a step; its pages are asked for at once
+  auto seek = [&](bool fresh) {
+    for (;; fresh = false) {
+      if (!fresh) {
+        const int units = WarpKeys(ahead, warp).units;
+        __syncwarp();
+        if (lane == 0) next_tile<MT, UK>(a, ahead, units);
+        __syncwarp();
+      }
+      l_more = ahead.left > 0;
+      if (!l_more) return;
+      const WarpKeys w(ahead, warp);
+      if (w.steps == 0) continue;
+      l_i = 0, l_steps = w.steps, l_k0 = w.k0, l_end = w.end, l_hk = ahead.hk;
+      l_table = a.b.table + ahead.b * a.b.table_stride;
+      fetch_pages();
+      return;
+    }
+  };
+  uint32_t ok_ring = 0;  // two bits a stage: the step's halves have a page
+  auto load = [&](int stage) {
+    if (l_more) {
+      const int j = l_k0 + l_i * UK;
+      int a0 = __shfl_sync(0xffffffffu, pg0, l_i & 31), a1 = __shfl_sync(0xffffffffu, pg1, l_i & 31);
+      if (static_cast<uint32_t>(a0) >= static_cast<uint32_t>(a.b.n_pages) ||
+          static_cast<uint32_t>(a1) >= static_cast<uint32_t>(a.b.n_pages)) {
+        if (lane == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+        if (a0 >= a.b.n_pages) a0 = -1;
+        if (a1 >= a.b.n_pages) a1 = -1;
+      }
+      ok_ring = (ok_ring & ~(3u << (2 * stage))) | ((a0 >= 0 ? 1u : 0u) | (a1 >= 0 ? 2u : 0u)) << (2 * stage);
+      const uint32_t dst = ring + stage * 2 * S::PLANE;
+      constexpr int RPI = 32 / CH;  // rows an instruction covers
+      const int c = lane % CH;
+#pragma unroll
+      for (int n = 0; n < STEP / RPI; ++n) {
+        const int r = n * RPI + lane / CH;
+        const int page = r < 8 ? a0 : a1;
+        const bool in = j + r < l_end && page >= 0;
+        const int64_t off = in ? kv_offset(a.b, page, l_hk, j + r) + 8 * c : 0;
+        const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
+        cp_async16(at, static_cast<const uint16_t*>(a.k) + off, in ? 16u : 0u);
+        cp_async16(at + S::PLANE, static_cast<const uint16_t*>(a.v) + off, in ? 16u : 0u);
+      }
+      if (++l_i == l_steps)
+        seek(false);
+      else if ((l_i & 31) == 0)
+        fetch_pages();
+    }
+    cp_commit();
+  };
+  seek(true);
+  load(0);
+  int stage = 0;
 
-    // Q as the A operand: rows g and g + 8, the same for every step
-    uint32_t qf[KS][4];
-    int top[2], bot[2];  // keys bot < j <= top are seen by the row
+  // Q as the A operand: rows g and g + 8 of the tile, the same for every step
+  uint32_t qf[KS][4];
+  auto load_q = [&]() {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int r = x.r0 + g + 8 * half;
-      const bool in = r < x.r1;
-      top[half] = in ? base + r / a.group : -1;
-      bot[half] = a.window > 0 ? top[half] - a.window : -1;
+      const int r = cur.x.r0 + g + 8 * half;
+      const bool in = r < cur.x.r1;
       const uint16_t* row =
           static_cast<const uint16_t*>(a.q) + (in ? row_offset(cur.s, a.group, cur.hk, r, a.ldq, D) : 0);
 #pragma unroll
@@ -102,60 +176,30 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
         qf[i][2 + half] = in ? *reinterpret_cast<const uint32_t*>(row + 16 * i + 8 + p2) : 0u;
       }
     }
+  };
+  load_q();
 
-    // steps of this warp: keys k0 + i * UK .. + 15
-    const int k0 = first + warp * STEP;
-    const int steps = end > k0 ? (end - k0 + UK - 1) / UK : 0;
-    // lane l holds the pages of step 32 * (i / 32) + l: its first and its second eight keys
-    int pg0 = -1, pg1 = -1;
-    const int32_t* table = a.b.table + cur.b * a.b.table_stride;
-    auto fetch_pages = [&](int i) {
-      const int j = k0 + (i + lane) * UK;
-      pg0 = pg1 = -1;
-      if (j < end) {
-        pg0 = table[j >> a.b.page_shift];
-        pg1 = j + 8 < end ? table[(j + 8) >> a.b.page_shift] : pg0;
-        if (pg0 < 0 || pg0 >= a.b.n_pages || pg1 < 0 || pg1 >= a.b.n_pages) {
-          flag_status(a.b.status, DEV_BAD_BATCH);
-          if (pg0 < 0 || pg0 >= a.b.n_pages) pg0 = -1;
-          if (pg1 < 0 || pg1 >= a.b.n_pages) pg1 = -1;
-        }
-      }
-    };
-    uint32_t ok_ring = 0;  // two bits a stage: the step's halves have a page
-    auto load = [&](int i, int stage) {
-      if (i < steps) {
-        if ((i & 31) == 0) fetch_pages(i);
-        const int j = k0 + i * UK;
-        const int a0 = __shfl_sync(0xffffffffu, pg0, i & 31), a1 = __shfl_sync(0xffffffffu, pg1, i & 31);
-        ok_ring = (ok_ring & ~(3u << (2 * stage))) | ((a0 >= 0 ? 1u : 0u) | (a1 >= 0 ? 2u : 0u)) << (2 * stage);
-        const uint32_t dst = ring + stage * 2 * S::PLANE;
-        constexpr int RPI = 32 / CH;  // rows an instruction covers
-        const int c = lane % CH;
+  while (cur.left > 0) {
+    const Tile x = cur.x;
+    const WarpKeys w(cur, warp);
+    const int base = cur.s.ctx - cur.s.n;
+    int top[2], bot[2];  // keys bot < j <= top are seen by the row
 #pragma unroll
-        for (int n = 0; n < STEP / RPI; ++n) {
-          const int r = n * RPI + lane / CH;
-          const int page = r < 8 ? a0 : a1;
-          const bool in = j + r < end && page >= 0;
-          const int64_t off = in ? kv_offset(a.b, page, cur.hk, j + r) + 8 * c : 0;
-          const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
-          cp_async16(at, static_cast<const uint16_t*>(a.k) + off, in ? 16u : 0u);
-          cp_async16(at + S::PLANE, static_cast<const uint16_t*>(a.v) + off, in ? 16u : 0u);
-        }
-      }
-      cp_commit();
-    };
+    for (int half = 0; half < 2; ++half) {
+      const int r = x.r0 + g + 8 * half;
+      top[half] = r < x.r1 ? base + a.group.token(r) : -1;
+      bot[half] = a.window > 0 ? top[half] - a.window : -1;
+    }
 
     float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) load(i, i);
-    int stage = 0;
-    for (int i = 0; i < steps; ++i) {
-      cp_wait<STAGES - 2>();
-      __syncwarp();  // every lane's copies have landed, and the stage refilled next has been read
-      load(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    for (int i = 0; i < w.steps; ++i) {
+      const uint32_t ok = (ok_ring >> (2 * stage)) & 3u;
+      __syncwarp();  // the stage refilled next has been read by every lane
+      load(stage ^ 1);
+      cp_wait<1>();
+      __syncwarp();  // every lane's copies have landed
       const uint32_t kb = ring + stage * 2 * S::PLANE, vb = kb + S::PLANE;
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       {
@@ -168,8 +212,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
           mma16816<CT>(s[1], qf[ks], f[2], f[3]);
         }
       }
-      const int j = k0 + i * UK;
-      const uint32_t ok = (ok_ring >> (2 * stage)) & 3u;
+      const int j = w.k0 + i * UK;
       float mx[2] = {m[0], m[1]};
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -216,17 +259,16 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
           }
         }
       }
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      stage ^= 1;
     }
-    cp_wait<0>();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
     }
-    __syncthreads();  // every warp is done with its ring
-    float* jo = reinterpret_cast<float*>(sm);
+    float* jo = reinterpret_cast<float*>(sm + S::RING);
     float* jm = jo + WARPS * MT * S::PITCH;  // [WARPS][MT][2]
+    __syncthreads();                         // the previous tile's results have been read
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = g + 8 * half;
@@ -239,31 +281,35 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
           *reinterpret_cast<float2*>(jm + (warp * MT + r) * 2) = make_float2(m[half], l[half]);
       }
     }
+    const SeqView seq = cur.s;
+    const int hk = cur.hk, first_u = cur.u;
+    next_tile<MT, UK>(a, cur, w.units);
+    if (cur.left > 0) load_q();  // arrives while the tile's results are joined
     __syncthreads();
-    const bool whole = units == x.units;
-    const int slot = 2 * blockIdx.x + (cur.u == 0 ? 1 : 0);
+    const bool whole = w.units == x.units;
+    const int slot = 2 * blockIdx.x + (first_u == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < (x.r1 - x.r0) * (D / 4); i += WARPS * 32) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
       float mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, jm[(w * MT + r) * 2]);
+      for (int i2 = 0; i2 < WARPS; ++i2) mm = fmaxf(mm, jm[(i2 * MT + r) * 2]);
       const float ref = mm == -INFINITY ? 0.f : mm;
       float ll = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float2 ml = *reinterpret_cast<const float2*>(jm + (w * MT + r) * 2);
+      for (int i2 = 0; i2 < WARPS; ++i2) {
+        const float2 ml = *reinterpret_cast<const float2*>(jm + (i2 * MT + r) * 2);
         const float f = fast_exp2(ml.x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(jo + (w * MT + r) * S::PITCH + c);
+        const float4 v = *reinterpret_cast<const float4*>(jo + (i2 * MT + r) * S::PITCH + c);
         ll += f * ml.y;
         acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
       }
       if (whole) {
         const float inv = ll > 0.f ? __fdiv_rn(1.f, ll) : 0.f;
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-        store_out4<CT>(a, row_offset(cur.s, a.group, cur.hk, x.r0 + r, a.ldo, D) + c, acc);
+        store_out4<CT>(a, row_offset(seq, a.group, hk, x.r0 + r, a.ldo, D) + c, acc);
         if (a.lse && c == 0)
-          a.lse[row_offset(cur.s, a.group, cur.hk, x.r0 + r, a.n_heads, 1)] =
+          a.lse[row_offset(seq, a.group, hk, x.r0 + r, a.n_heads, 1)] =
               ll > 0.f ? mm * LN2 + logf(ll) : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(a.part + part_offset<MT, D>(slot, r, c)) = acc;
@@ -274,10 +320,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
         }
       }
     }
-    __syncthreads();  // the ring is free again
-    next_tile<MT, UK>(a, cur, units);
   }
-  pdl_launch_dependents();
 }
 
 template <int CT, int D>

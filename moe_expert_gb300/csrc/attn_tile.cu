@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
         const bool in = r < cur.x.r1;
         const int first = cur.x.lo + cur.u * UK, end = cur.x.hi;
         const int32_t* table = a.b.table + cur.b * a.b.table_stride;
-        const int top = in ? cur.s.ctx - cur.s.n + r / a.group : -1;
+        const int top = in ? cur.s.ctx - cur.s.n + a.group.token(r) : -1;
         const int bot = a.window > 0 ? top - a.window : -1;
         float m = -INFINITY, l = 0.f;
         // lane c < 16: the page of keys j + 8 c .. + 7 of a block, read a block ahead (0 where there is no such key)
