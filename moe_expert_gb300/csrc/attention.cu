@@ -7,18 +7,22 @@
 namespace moex {
 
 // Tiles that ranges cut, one column of CTAs for each range that begins inside a
-// tile and is the first to do so, a CTA for 32 rows: the partials in the order of
+// tile and is the first to do so, a CTA for 16 rows: the partials in the order of
 // their keys, FP32.  CTA c of the first kernel leaves its first tile in slot 2c
 // when it begins inside it, and its last in slot 2c + 1 when it does not finish
 // it.  Latency bounds this kernel, so the rows' weights of up to 32 partials are
 // formed first and the partials then read independently of one another.
+constexpr int JOIN_ROWS = 16;
+
 template <int CT, int D, int MT>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a) {
-  constexpr int R = MT < 32 ? MT : 32, F = 32, V = D / 4, ITEMS = R * V / 128;
-  __shared__ float2 ml[F][R];          // (maximum, sum), then (weight, sum)
+__global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const AttnArgs a) {
+  constexpr int R = JOIN_ROWS, F = 32, V = D / 4, WARPS = R * V / 32;  // a thread: four columns of a row
+  __shared__ float weight[F][R + 1];
+  __shared__ int slots[F];
   __shared__ float rescale[R], total[R], top[R];
   __shared__ float4 rows[R][V + 1];
   const int n_cta = gridDim.x, r0 = blockIdx.y * R;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   const RangeStart x = a.plan[blockIdx.x];
@@ -29,76 +33,67 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a) {
   // with fewer units than CTAs a range is one unit or none
   const bool sparse = x.W < n_cta;
   const int parts = sparse ? x.units : static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta)) - c0 + 1;
-  auto slot_of = [&](int f) -> int64_t {
-    const int64_t c = sparse ? range_of(x.tile_u + f, x.W, n_cta) : c0 + f;
-    return 2 * c + (f == 0 ? 1 : 0);
-  };
-  const int nr = min(R, x.rows - r0);
+  const int nr = min(R, x.rows - r0), row = threadIdx.x % R;  // and columns 4 (threadIdx.x / R)
   const float* stats = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
-  float4 acc[ITEMS];
-#pragma unroll
-  for (int k = 0; k < ITEMS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* part = a.part + part_offset<MT, D>(0, r0 + row, 4 * (threadIdx.x / R));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
   for (int f0 = 0; f0 < parts; f0 += F) {
     const int nf = min(F, parts - f0);
-    for (int i = threadIdx.x; i < nf * R; i += 128)
-      if (i % R < nr)
-        ml[i / R][i % R] = *reinterpret_cast<const float2*>(stats + 2 * (slot_of(f0 + i / R) * MT + r0 + i % R));
+    if (threadIdx.x < nf) {
+      const int f = f0 + threadIdx.x;
+      const int c = sparse ? static_cast<int>(range_of(x.tile_u + f, x.W, n_cta)) : c0 + f;
+      slots[threadIdx.x] = 2 * c + (f == 0 ? 1 : 0);
+    }
     __syncthreads();
-    if (threadIdx.x < nr) {
-      const int r = threadIdx.x;
+    // a warp a row, a lane a partial
+#pragma unroll 1
+    for (int r = warp; r < nr; r += WARPS) {
+      float2 p = make_float2(-INFINITY, 0.f);
+      if (lane < nf)
+        p = *reinterpret_cast<const float2*>(stats + 2 * (static_cast<int64_t>(slots[lane]) * MT + r0 + r));
       const float old = f0 ? top[r] : -INFINITY;
-      float m = old, l = 0.f;
-      for (int f = 0; f < nf; ++f) m = fmaxf(m, ml[f][r].x);
-      const float ref = m == -INFINITY ? 0.f : m;
-      for (int f = 0; f < nf; ++f) {
-        const float w = fast_exp2(ml[f][r].x - ref);
-        l += w * ml[f][r].y;
-        ml[f][r].x = w;
+      float m = fmaxf(old, p.x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float ref = m == -INFINITY ? 0.f : m, wt = fast_exp2(p.x - ref);
+      float l = wt * p.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      weight[lane][r] = wt;
+      if (lane == 0) {
+        const float k = fast_exp2(old - ref);
+        rescale[r] = k;
+        total[r] = (f0 ? total[r] * k : 0.f) + l;
+        top[r] = m;
       }
-      const float k = fast_exp2(old - ref);
-      rescale[r] = k;
-      total[r] = (f0 ? total[r] * k : 0.f) + l;
-      top[r] = m;
     }
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int r = (threadIdx.x + 128 * k) % R;
-      const float old = r < nr ? rescale[r] : 0.f;
-      acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
-    }
+    if (row < nr) {
+      const float old = rescale[row];
+      acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
 #pragma unroll 4
-    for (int f = 0; f < nf; ++f) {
-      const float* part = a.part + part_offset<MT, D>(slot_of(f0 + f), r0, 0);
-#pragma unroll
-      for (int k = 0; k < ITEMS; ++k) {
-        const int i = threadIdx.x + 128 * k;  // columns 4 (i / R) of row i % R
-        if (i % R < nr) {
-          const float4 v = *reinterpret_cast<const float4*>(part + 4 * i);
-          const float w = ml[f][i % R].x;
-          acc[k].x += w * v.x, acc[k].y += w * v.y, acc[k].z += w * v.z, acc[k].w += w * v.w;
-        }
+      for (int f = 0; f < nf; ++f) {
+        const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(slots[f]) * MT * D);
+        const float wt = weight[f][row];
+        acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
       }
     }
     __syncthreads();
   }
   // by way of shared memory, so that a row is written in one piece
-#pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const int i = threadIdx.x + 128 * k;
-    rows[i % R][i / R] = acc[k];
-  }
+  rows[row][threadIdx.x / R] = acc;
   __syncthreads();
+  const int r = threadIdx.x / V, c = threadIdx.x % V;
+  if (r >= nr) return;
   const SeqView s = seq_view(a.b, x.b);
-  for (int i = threadIdx.x; i < nr * V; i += 128) {
-    const int r = i / V, row = x.t * MT + r0 + r;
-    const float l = total[r], inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
-    float4 v = rows[r][i % V];
-    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-    store_out4<CT>(a, row_offset(s, a.group, x.hk, row, a.ldo, D) + 4 * (i % V), v);
-    if (a.lse && i % V == 0)
-      a.lse[row_offset(s, a.group, x.hk, row, a.n_heads, 1)] = l > 0.f ? top[r] * LN2 + logf(l) : -INFINITY;
-  }
+  const float l = total[r], inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+  float4 v = rows[r][c];
+  v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+  store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r0 + r, a.ldo, D) + 4 * c, v);
+  if (a.lse && c == 0)
+    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r0 + r, a.n_heads, 1)] =
+        l > 0.f ? top[r] * LN2 + logf(l) : -INFINITY;
 }
 
 namespace {
@@ -128,8 +123,9 @@ HeadGroup head_group(int n, int n_tokens) {
 
 template <int CT, int D>
 cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
-  if (g.tile) return launch_pdl(attend_join_kernel<CT, D, TILE_MT>, dim3(g.ctas, TILE_MT / 32), dim3(128), 0, s, a);
-  return launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, dim3(g.ctas), dim3(128), 0, s, a);
+  const dim3 grid(g.ctas, g.mt / JOIN_ROWS), block(JOIN_ROWS * D / 4);
+  return g.tile ? launch_pdl(attend_join_kernel<CT, D, TILE_MT>, grid, block, 0, s, a)
+                : launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, grid, block, 0, s, a);
 }
 
 }  // namespace

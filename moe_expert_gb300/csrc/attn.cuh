@@ -9,7 +9,10 @@
 // CTA c of G takes units floor(c W / G) .. floor((c+1) W / G) of W, whatever the
 // lengths.  A tile inside one range is finished by its CTA; one that crosses a
 // border leaves FP32 partials (unnormalised output, maximum, sum) in the
-// workspace, which a second kernel joins in the order of the keys.
+// workspace, which a second kernel joins in the order of the keys.  Starting a
+// tile costs about as much as some units (its queries, its output), so every
+// tile counts DEAD units more than it has, in front of its own: the share of a
+// CTA with many short tiles holds fewer keys.
 #pragma once
 
 #include "batch.cuh"
@@ -31,7 +34,7 @@ struct HeadGroup {
 
 // Where a CTA's range begins, for the kernel that joins the tiles cut there.
 struct RangeStart {
-  int64_t W, tile_u;     // units of the batch; units before the tile
+  int64_t W, tile_u;     // units of the batch; units before the tile's own
   int b, hk, t, u;       // sequence, key head, tile, unit inside the tile
   int units, rows;       // of the tile
 };
@@ -79,12 +82,21 @@ __device__ __forceinline__ Tile tile_of(const SeqView& s, const HeadGroup& group
   return x;
 }
 
-// Units of a sequence and key head, the warp's lanes taking tiles in turn.
-template <int MT, int UK>
+// Units of a sequence and key head: few tiles by one thread; many by a warp,
+// its lanes taking them in turn.
+constexpr int FEW_TILES = 6;
+template <int MT, int UK, int DEAD>
+__device__ __forceinline__ int seq_units_few(const SeqView& s, const HeadGroup& group, int window) {
+  int u = 0;
+#pragma unroll 1
+  for (int t = 0; t * MT < s.n * group.n; ++t) u += tile_of<MT, UK>(s, group, window, t).units + DEAD;
+  return u;
+}
+template <int MT, int UK, int DEAD>
 __device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, const HeadGroup& group, int window) {
   const int tiles = (s.n * group.n + MT - 1) / MT;
   int64_t u = 0;
-  for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_of<MT, UK>(s, group, window, t).units;
+  for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_of<MT, UK>(s, group, window, t).units + DEAD;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   return u;
@@ -103,7 +115,7 @@ __device__ __forceinline__ int64_t range_of(int64_t u, int64_t W, int G) {
 
 // Where a CTA is in the list of units.
 struct Cursor {
-  int64_t left;    // units of this CTA's range still to do, from here on
+  int64_t left;    // units of this CTA's range from here on, the next tile's dead ones taken off
   int b, hk, t, u; // sequence, key head, tile, unit inside the tile
   SeqView s;
   Tile x;
@@ -112,7 +124,7 @@ struct Cursor {
 // Every CTA finds the batch's number of units and its own range: a scan over
 // the sequences, THREADS at a time.  The cursor is at the range's first unit,
 // and so is the CTA's entry of the plan.
-template <int MT, int UK, int THREADS>
+template <int MT, int UK, int DEAD, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
   __shared__ int64_t warp_sum[2][THREADS / 32];
   __shared__ int64_t found[2];  // units before the sequence, its units
@@ -122,21 +134,24 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   int64_t total = 0, mine = 0, before = 0;
   SeqView s{0, 0, 0, false};
   // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
     int64_t run = 0;
     for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
       const int b = base + threadIdx.x;
       if (pass == 0 || a.b.n_seqs > THREADS) {
-        // a thread a sequence; one of several tiles is counted by the whole warp
+        // a thread a sequence; one of many tiles is counted by the whole warp
         s = SeqView{0, 0, 0, false};
         if (b < a.b.n_seqs) s = seq_view(a.b, b);
         if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-        int64_t v = s.n > 0 ? tile_of<MT, UK>(s, a.group, a.window, 0).units : 0;
-        for (uint32_t many = __ballot_sync(0xffffffffu, s.n * a.group.n > MT); many; many &= many - 1) {
+        const bool few = s.n * a.group.n <= FEW_TILES * MT;
+        int64_t v = few ? seq_units_few<MT, UK, DEAD>(s, a.group, a.window) : 0;
+#pragma unroll 1
+        for (uint32_t many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
           const int src = __ffs(many) - 1;
           SeqView w{0, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.ctx, src), false};
-          const int64_t u = seq_units_warp<MT, UK>(w, a.group, a.window);
+          const int64_t u = seq_units_warp<MT, UK, DEAD>(w, a.group, a.window);
           if (lane == src) v = u;
         }
         v *= a.n_kv_heads;
@@ -145,10 +160,20 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         const int warps = min((a.b.n_seqs - base + 31) / 32, THREADS / 32);
         int64_t x = v;
         if (warp < warps) {
+          if (__any_sync(0xffffffffu, v >> 25)) {
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+              const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+              if (lane >= o) x += y;
+            }
+          } else {  // the warp's sum fits 32 bits
+            int x32 = static_cast<int>(v);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, x32, o);
+              if (lane >= o) x32 += y;
+            }
+            x = x32;
           }
           if (lane == 31) warp_sum[it & 1][warp] = x;
         }
@@ -188,11 +213,12 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   off -= cur.hk * per;
   cur.t = 0;
   // the tile: 32 at a time, every warp for itself
+#pragma unroll 1
   for (int t0 = 0; cur.s.n * a.group.n > MT; t0 += 32) {
     const int t = t0 + lane;
-    int n = t * MT < cur.s.n * a.group.n ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units : 0;
+    const int n = t * MT < cur.s.n * a.group.n ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units + DEAD : 0;
     int64_t sum = n;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
@@ -207,15 +233,18 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
     off -= __shfl_sync(0xffffffffu, sum, 31);
   }
   cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
-  cur.u = static_cast<int>(off);
+  const int64_t tile_u = u0 - off + DEAD;
+  off -= DEAD;
+  if (off < 0) cur.left += off;  // the range begins among the tile's dead units
+  cur.u = static_cast<int>(max(off, int64_t(0)));
   if (threadIdx.x == 0)
-    a.plan[cta] = RangeStart{total, u0 - off, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0};
+    a.plan[cta] = RangeStart{total, tile_u, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0};
 }
 
 // To the first unit of the next tile; `done` units of this one were in the range.
-template <int MT, int UK>
+template <int MT, int UK, int DEAD>
 __device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int done) {
-  cur.left -= done;
+  cur.left -= done + DEAD;
   cur.u = 0;
   if (cur.left <= 0) return;
   ++cur.t;

@@ -8,10 +8,10 @@ namespace moex {
 struct AttnArgs;
 
 // Few rows a key head: tiles of 16 rows, units of 64 keys, two CTAs an SM.
-constexpr int STREAM_MT = 16, STREAM_UK = 64, STREAM_CTAS_PER_SM = 2;
+constexpr int STREAM_MT = 16, STREAM_UK = 64, STREAM_DEAD = 2, STREAM_CTAS_PER_SM = 2;
 
 // Many rows a key head: tiles of 256 rows, units of 128 keys, one CTA an SM.
-constexpr int TILE_MT = 256, TILE_UK = 128;
+constexpr int TILE_MT = 256, TILE_UK = 128, TILE_DEAD = 2;
 // The hint (new tokens of the longest sequence x heads a key head) above which tiles are taken.
 constexpr int TILE_MIN_ROWS = 32;
 

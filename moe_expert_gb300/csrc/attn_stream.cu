@@ -15,7 +15,7 @@
 namespace moex {
 namespace {
 
-constexpr int MT = STREAM_MT, UK = STREAM_UK;
+constexpr int MT = STREAM_MT, UK = STREAM_UK, DEAD = STREAM_DEAD;
 constexpr int WARPS = 4, STEP = 16, STAGES = 2;
 static_assert(UK == WARPS * STEP, "a unit is one step of every warp");
 
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   pdl_wait();
   pdl_launch_dependents();  // the joining kernel's CTAs fit beside these, and wait
   Cursor cur;
-  find_range<MT, UK, WARPS * 32>(a, blockIdx.x, gridDim.x, cur);
+  find_range<MT, UK, DEAD, WARPS * 32>(a, blockIdx.x, gridDim.x, cur);
   if (cur.left <= 0) return;
   const uint32_t ring = smem_u32(sm) + warp * STAGES * 2 * S::PLANE;
 
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
       if (!fresh) {
         const int units = WarpKeys(ahead, warp).units;
         __syncwarp();
-        if (lane == 0) next_tile<MT, UK>(a, ahead, units);
+        if (lane == 0) next_tile<MT, UK, DEAD>(a, ahead, units);
         __syncwarp();
       }
       l_more = ahead.left > 0;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
     }
     const SeqView seq = cur.s;
     const int hk = cur.hk, first_u = cur.u;
-    next_tile<MT, UK>(a, cur, w.units);
+    next_tile<MT, UK, DEAD>(a, cur, w.units);
     if (cur.left > 0) load_q();  // arrives while the tile's results are joined
     __syncthreads();
     const bool whole = w.units == x.units;

@@ -23,7 +23,7 @@
 namespace moex {
 namespace {
 
-constexpr int MT = TILE_MT, UK = TILE_UK;
+constexpr int MT = TILE_MT, UK = TILE_UK, DEAD = TILE_DEAD;
 constexpr int THREADS = 512;
 constexpr float GROW = 8.f;  // log2 of the growth of a maximum that rescales O
 
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
   Cursor& cur = cursors[warp];
   {
     Cursor at;
-    find_range<MT, UK, THREADS>(a, blockIdx.x, gridDim.x, at);
+    find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at);
     if (lane == 0) cur = at;
   }
   tc_fence_before();
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
   };
   auto advance = [&](int units) {
     __syncwarp();
-    if (lane == 0) next_tile<MT, UK>(a, cur, units);
+    if (lane == 0) next_tile<MT, UK, DEAD>(a, cur, units);
     __syncwarp();
   };
 
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             m = mn;
             l *= f;
             if (i > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
                 tmem_ld16(to + 16 * q, o);
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
         const float inv = whole ? (l > 0.f ? __fdiv_rn(1.f, l) : 0.f) : 1.f;
         const int64_t off = in ? row_offset(cur.s, a.group, cur.hk, r, a.ldo, D) : -1;
         float* part = a.part + part_offset<MT, D>(slot, row, 0);
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(to + 32 * q, o);
