@@ -129,9 +129,15 @@ def _check(status: int, what: str):
         raise MoexError(status, what)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _raw_stream = None
@@ -421,30 +427,43 @@ def moe_decode_noalloc(gate_up: PackedWeight, down: PackedWeight, x, ids, w, out
     return out
 
 
-_type_codes = None
+_type_codes = {}
 
 
 def _type(dtype) -> int:
     """moex_type of a torch dtype."""
-    global _type_codes
-    if _type_codes is None:
+    if not _type_codes:
         torch = _torch()
-        _type_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        _type_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     code = _type_codes.get(dtype)
     if code is None:
         raise TypeError(f"expected float32, bfloat16 or float16, got {dtype}")
     return code
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _rows(t, shape, what: str) -> int:
+    """Row stride of a CUDA matrix of `shape` with contiguous rows (its width
+    for a single row, whose stride says nothing)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
+    if t.shape != shape or t.stride(1) != 1:
+        raise ValueError(f"{what}: expected rows of shape {tuple(shape)}, contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
-def _on_gpu(*tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor has to be a CUDA tensor")
+def _flat(t, numel: int, dtype, what: str) -> int:
+    """Pointer of a contiguous CUDA tensor of `numel` elements of `dtype`."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
+    if t.numel() != numel or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {numel} contiguous elements of {dtype}")
+    return t.data_ptr()
+
+
+def _float_rows(t, shape, what: str) -> int:
+    if t.dtype != _torch().float32:
+        raise ValueError(f"{what}: expected float32")
+    return _rows(t, shape, what)
 
 
 def add_rms_norm(x, gamma, eps: float = 1e-6, residual=None, sum_out=None, y=None, y_dtype=None, quantize=False,
@@ -457,40 +476,34 @@ def add_rms_norm(x, gamma, eps: float = 1e-6, residual=None, sum_out=None, y=Non
     given, q int8 [T, H] and ds float32 [T, H/32, 2] with quantize=True (the
     q8_1 rows that qgemv takes); None for what was not asked for."""
     torch = _torch()
-    T, H = x.shape
-    _need(x.stride(1) == 1 and gamma.dtype == torch.float32 and gamma.numel() == H and gamma.is_contiguous(),
-          "x rows contiguous, gamma float32 [H]")
+    shape = x.shape
+    T, H = shape
+    ldx, xt = _rows(x, shape, "x"), _type(x.dtype)
+    r_ptr = s_ptr = y_ptr = q_ptr = ds_ptr = None
+    ldr = lds = ldy = yt = 0
     if residual is not None:
-        _need(residual.shape == x.shape and residual.dtype == torch.float32 and residual.stride(1) == 1,
-              "residual: float32 [T, H]")
+        ldr, r_ptr = _float_rows(residual, shape, "residual"), residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+            sum_out = torch.empty(shape, dtype=torch.float32, device=x.device)
     if sum_out is not None:
-        _need(sum_out.shape == x.shape and sum_out.dtype == torch.float32 and sum_out.stride(1) == 1,
-              "sum_out: float32 [T, H]")
+        lds, s_ptr = _float_rows(sum_out, shape, "sum_out"), sum_out.data_ptr()
     if y is None and y_dtype is not None:
-        y = torch.empty((T, H), dtype=y_dtype, device=x.device)
+        y = torch.empty(shape, dtype=y_dtype, device=x.device)
     if y is not None:
-        _need(y.shape == x.shape and y.stride(1) == 1, "y: [T, H]")
+        ldy, yt, y_ptr = _rows(y, shape, "y"), _type(y.dtype), y.data_ptr()
     if quantize:
         if q is None:
-            q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+            q = torch.empty(shape, dtype=torch.int8, device=x.device)
         if ds is None:
             ds = torch.empty((T, H // QK, 2), dtype=torch.float32, device=x.device)
-        _need(q.numel() == T * H and q.dtype == torch.int8 and q.is_contiguous() and ds.numel() == T * H // QK * 2
-              and ds.dtype == torch.float32 and ds.is_contiguous(), "q: int8 [T, H], ds: float32 [T, H/32, 2]")
+        q_ptr = _flat(q, T * H, torch.int8, "q")
+        ds_ptr = _flat(ds, T * (H // QK) * 2, torch.float32, "ds")
     else:
         q = ds = None
-    _on_gpu(x, gamma, residual, sum_out, y, q, ds)
-    _check(lib().moex_add_rms_norm(
-        x.data_ptr(), _type(x.dtype), x.stride(0) if T > 1 else H,
-        None if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0) if T > 1 else H,
-        gamma.data_ptr(), eps, T, H,
-        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0) if T > 1 else H,
-        None if y is None else y.data_ptr(), 0 if y is None else _type(y.dtype),
-        0 if y is None else y.stride(0) if T > 1 else H,
-        None if q is None else q.data_ptr(), None if q is None else ds.data_ptr(), _stream(stream)),
-        "moex_add_rms_norm")
+    st = lib().moex_add_rms_norm(x.data_ptr(), xt, ldx, r_ptr, ldr, _flat(gamma, H, torch.float32, "gamma"), eps, T, H,
+                                 s_ptr, lds, y_ptr, yt, ldy, q_ptr, ds_ptr, _stream(stream))
+    if st:
+        _check(st, "moex_add_rms_norm")
     return sum_out, y, q, ds
 
 
@@ -501,11 +514,10 @@ def dequantize_q8_1(q, ds, y=None, dtype=None, stream=None):
     T, K = q.shape
     if y is None:
         y = torch.empty((T, K), dtype=dtype or torch.float32, device=q.device)
-    _need(q.is_contiguous() and ds.is_contiguous() and y.is_contiguous() and y.shape == q.shape
-          and ds.numel() == T * K // QK * 2, "q, ds, y: contiguous [T, K], [T, K/32, 2], [T, K]")
-    _on_gpu(q, ds, y)
-    _check(lib().moex_dequantize_q8_1(q.data_ptr(), ds.data_ptr(), T, K, y.data_ptr(), _type(y.dtype),
-                                      _stream(stream)), "moex_dequantize_q8_1")
+    st = lib().moex_dequantize_q8_1(_flat(q, T * K, torch.int8, "q"), _flat(ds, T * (K // QK) * 2, torch.float32, "ds"),
+                                    T, K, _flat(y, T * K, y.dtype, "y"), _type(y.dtype), _stream(stream))
+    if st:
+        _check(st, "moex_dequantize_q8_1")
     return y
 
 
@@ -521,43 +533,54 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
     and w float32 [T, k], as moe_decode and moe_prefill take them."""
     torch = _torch()
     T, E = logits.shape
-    _need(score in SCORE, "score: softmax or sigmoid")
-    _need(logits.stride(1) == 1, "logits rows contiguous")
-    _need(bias is None or (bias.numel() == E and bias.dtype == torch.float32 and bias.is_contiguous()),
-          "bias: float32 [E]")
+    code = SCORE.get(score)
+    if code is None:
+        raise ValueError("score: softmax or sigmoid")
+    ldl = _rows(logits, logits.shape, "logits")
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     if w is None:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous()
-          and w.shape == (T, k) and w.dtype == torch.float32 and w.is_contiguous(), "ids: int32 [T, k], w: float32 [T, k]")
-    _on_gpu(logits, bias, ids, w)
-    _check(lib().moex_route_experts(logits.data_ptr(), _type(logits.dtype), logits.stride(0) if T > 1 else E,
-                                    None if bias is None else bias.data_ptr(), T, E, k, SCORE[score], groups,
-                                    top_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(),
-                                    _stream(stream)), "moex_route_experts")
+    st = lib().moex_route_experts(logits.data_ptr(), _type(logits.dtype), ldl,
+                                  None if bias is None else _flat(bias, E, torch.float32, "bias"), T, E, k, code,
+                                  groups, top_groups, group_top, 1 if renorm else 0, scale,
+                                  _flat(ids, T * k, torch.int32, "ids"), _flat(w, T * k, torch.float32, "w"),
+                                  _stream(stream))
+    if st:
+        _check(st, "moex_route_experts")
     return ids, w
 
 
 def _paged_kv(k_cache, v_cache) -> PagedKV:
+    if not (k_cache.is_cuda and v_cache.is_cuda):
+        raise ValueError("k_cache, v_cache: every tensor has to be a CUDA tensor")
     n_pages, heads, page, dim = k_cache.shape
     st = k_cache.stride()
-    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype and v_cache.stride() == st and st[3] == 1,
-          "k_cache and v_cache: the same type, shape [pages, heads, page, dim] and strides, dim contiguous")
+    if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.stride() != st or st[3] != 1):
+        raise ValueError("k_cache and v_cache: the same type, shape [pages, heads, page, dim] and strides, dim contiguous")
     return PagedKV(_type(k_cache.dtype), page, heads, dim, n_pages, st[0], st[1], st[2], k_cache.data_ptr(),
                    v_cache.data_ptr())
 
 
 def _batch(cu_q, ctx_len, page_table, n_tokens, max_q) -> Batch:
     i32 = _torch().int32
-    n = ctx_len.numel()
-    _need(cu_q.dtype == i32 and ctx_len.dtype == i32 and page_table.dtype == i32 and cu_q.numel() == n + 1
-          and page_table.dim() == 2 and page_table.shape[0] == n and page_table.stride(1) == 1
-          and cu_q.is_contiguous() and ctx_len.is_contiguous(),
-          "cu_q: int32 [B + 1], ctx_len: int32 [B], page_table: int32 [B, width]")
-    width = page_table.shape[1]
+    n, width = page_table.shape
+    if not page_table.is_cuda:
+        raise ValueError("page_table: every tensor has to be a CUDA tensor")
+    if page_table.dtype != i32 or page_table.stride(1) != 1:
+        raise ValueError("page_table: expected int32 [B, width], rows contiguous")
     return Batch(n, n_tokens, n_tokens if max_q is None else max_q, width, page_table.stride(0) if n > 1 else width,
-                 cu_q.data_ptr(), ctx_len.data_ptr(), page_table.data_ptr())
+                 _flat(cu_q, n + 1, i32, "cu_q"), _flat(ctx_len, n, i32, "ctx_len"), page_table.data_ptr())
+
+
+def _heads(t, T: int, heads: int, dim: int, what: str) -> int:
+    """Token stride of a CUDA tensor [T, heads, dim] whose tokens are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
+    st = t.stride()
+    if t.shape != (T, heads, dim) or st[2] != 1 or (st[1] != dim and heads > 1):
+        raise ValueError(f"{what}: expected [{T}, {heads}, {dim}], heads contiguous")
+    return st[0] if T > 1 else heads * dim
 
 
 def rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, n_heads: int, cos_sin=None,
@@ -575,24 +598,22 @@ def rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, n_heads: int
     T = qkv.shape[0]
     kv = _paged_kv(k_cache, v_cache)
     b = _batch(cu_q, ctx_len, page_table, T, None)
-    _need(qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] == (n_heads + 2 * kv.n_kv_heads) * kv.head_dim,
-          "qkv: [T, (n_heads + 2 * kv_heads) * dim]")
-    rot = 0
+    heads, dim = kv.n_kv_heads, kv.head_dim
+    ld = _rows(qkv, (T, (n_heads + 2 * heads) * dim), "qkv")
+    rot = n_pos = 0
+    cs_ptr = None
     if cos_sin is not None:
-        _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous(),
-              "cos_sin: float32 [positions, rot_dim]")
-        rot = cos_sin.shape[1]
+        n_pos, rot = cos_sin.shape
+        cs_ptr = _flat(cos_sin, n_pos * rot, torch.float32, "cos_sin")
     if q is None:
-        q = torch.empty((T, n_heads, kv.head_dim), dtype=k_cache.dtype, device=qkv.device)
-    _need(q.shape == (T, n_heads, kv.head_dim) and q.dtype == k_cache.dtype and q.stride(2) == 1
-          and q.stride(1) == kv.head_dim, "q: [T, n_heads, dim] of the cache type, heads contiguous")
-    _on_gpu(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, cos_sin, q)
-    _check(lib().moex_rope_kv_write(qkv.data_ptr(), _type(qkv.dtype), qkv.stride(0) if T > 1 else qkv.shape[1],
-                                    ctypes.byref(kv), ctypes.byref(b), n_heads,
-                                    cos_sin.data_ptr() if rot else None, cos_sin.shape[0] if rot else 0, rot,
-                                    1 if interleaved else 0, q.data_ptr(),
-                                    q.stride(0) if T > 1 else n_heads * kv.head_dim, _stream(stream)),
-           "moex_rope_kv_write")
+        q = torch.empty((T, n_heads, dim), dtype=k_cache.dtype, device=qkv.device)
+    if q.dtype != k_cache.dtype:
+        raise ValueError("q: expected the cache's type")
+    st = lib().moex_rope_kv_write(qkv.data_ptr(), _type(qkv.dtype), ld, kv, b, n_heads, cs_ptr, n_pos, rot,
+                                  1 if interleaved else 0, q.data_ptr(), _heads(q, T, n_heads, dim, "q"),
+                                  _stream(stream))
+    if st:
+        _check(st, "moex_rope_kv_write")
     return q
 
 
@@ -600,7 +621,7 @@ def paged_attention_workspace_bytes(k_cache, v_cache, cu_q, ctx_len, page_table,
                                     max_q: Optional[int] = None) -> int:
     kv = _paged_kv(k_cache, v_cache)
     b = _batch(cu_q, ctx_len, page_table, n_tokens, max_q)
-    return int(lib().moex_paged_attention_workspace_bytes(ctypes.byref(kv), ctypes.byref(b), n_heads))
+    return int(lib().moex_paged_attention_workspace_bytes(kv, b, n_heads))
 
 
 def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optional[int] = None,
@@ -616,23 +637,27 @@ def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optio
     T, n_heads, dim = q.shape
     kv = _paged_kv(k_cache, v_cache)
     b = _batch(cu_q, ctx_len, page_table, T, max_q)
-    _need(q.dtype == k_cache.dtype and q.stride(2) == 1 and q.stride(1) == dim and dim == kv.head_dim,
-          "q: [T, n_heads, dim] of the cache type, heads contiguous")
+    if q.dtype != k_cache.dtype or dim != kv.head_dim:
+        raise ValueError("q: expected the cache's type and head size")
+    ldq = _heads(q, T, n_heads, dim, "q")
     if out is None:
         out = torch.empty((T, n_heads, dim), dtype=out_dtype or q.dtype, device=q.device)
-    _need(out.shape == q.shape and out.stride(2) == 1 and out.stride(1) == dim, "out: [T, n_heads, dim]")
-    _need(lse is None or (lse.shape == (T, n_heads) and lse.dtype == torch.float32 and lse.is_contiguous()),
-          "lse: float32 [T, n_heads]")
-    _on_gpu(q, k_cache, v_cache, cu_q, ctx_len, page_table, out, lse, ws)
+    ldo = _heads(out, T, n_heads, dim, "out")
     L = lib()
     if ws is None:
-        nbytes = L.moex_paged_attention_workspace_bytes(ctypes.byref(kv), ctypes.byref(b), n_heads)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    _check(L.moex_paged_attention(q.data_ptr(), q.stride(0) if T > 1 else n_heads * dim, ctypes.byref(kv),
-                                  ctypes.byref(b), n_heads, dim ** -0.5 if scale is None else scale, window,
-                                  out.data_ptr(), _type(out.dtype), out.stride(0) if T > 1 else n_heads * dim,
-                                  None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-                                  0 if ws is None else ws.numel(), _stream(stream)), "moex_paged_attention")
+        nbytes = L.moex_paged_attention_workspace_bytes(kv, b, n_heads)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    ws_ptr, nbytes = None, 0
+    if ws is not None:
+        nbytes = ws.numel()
+        ws_ptr = _flat(ws, nbytes, torch.uint8, "ws")
+    st = L.moex_paged_attention(q.data_ptr(), ldq, kv, b, n_heads, dim ** -0.5 if scale is None else scale, window,
+                                out.data_ptr(), _type(out.dtype), ldo,
+                                None if lse is None else _flat(lse, T * n_heads, torch.float32, "lse"), ws_ptr, nbytes,
+                                _stream(stream))
+    if st:
+        _check(st, "moex_paged_attention")
     return out
 
 

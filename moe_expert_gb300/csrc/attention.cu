@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
   __syncthreads();
   const int r = threadIdx.x / V, c = threadIdx.x % V;
   if (r >= nr) return;
-  const SeqView s = seq_view(a.b, x.b);
+  const SeqView s{x.first, x.n, x.ctx, false};
   const float l = total[r], inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
   float4 v = rows[r][c];
   v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;

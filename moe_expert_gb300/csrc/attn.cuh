@@ -37,6 +37,7 @@ struct RangeStart {
   int64_t W, tile_u;     // units of the batch; units before the tile's own
   int b, hk, t, u;       // sequence, key head, tile, unit inside the tile
   int units, rows;       // of the tile
+  int first, n, ctx, pad;  // of the sequence
 };
 
 struct AttnArgs {
@@ -201,7 +202,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   const int64_t u0 = range_begin(cta, total, n_cta);
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
   if (cur.left == 0) {
-    if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0};
+    if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   cur.b = found_b;
@@ -238,7 +239,8 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   if (off < 0) cur.left += off;  // the range begins among the tile's dead units
   cur.u = static_cast<int>(max(off, int64_t(0)));
   if (threadIdx.x == 0)
-    a.plan[cta] = RangeStart{total, tile_u, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0};
+    a.plan[cta] = RangeStart{total, tile_u, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0,
+                             cur.s.first, cur.s.n, cur.s.ctx, 0};
 }
 
 // To the first unit of the next tile; `done` units of this one were in the range.

@@ -13,7 +13,9 @@ struct RouteArgs {
   float* w;
   int64_t ldl;
   float scale;
-  int T, E, k, sigmoid, groups, top_groups, group_top, renorm, group_size;
+  int T, k, sigmoid, groups, top_groups, group_top, renorm, group_size;
+  int lane_shift;  // log2 of the lanes a group takes
+  int vec;         // rows can be read four at a time
 };
 
 // Ranks are compared as 32-bit keys whose unsigned order is the order of the
@@ -29,9 +31,23 @@ __device__ __forceinline__ float key_rank(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// One warp a token; lane l holds experts l + 32 i, i < PER (E <= 32 PER).
-// Arg-max rounds take the largest key by redux.sync and the lowest index
-// among the lanes that hold it.  FP32 throughout; expf and IEEE division.
+// Score of one logit; 0 for a masked one.  `top` and `sum` are the token's
+// largest logit and sum of exponentials (softmax).
+__device__ __forceinline__ float score_of(float x, int sigmoid, float top, float sum) {
+  if (!(x > -INFINITY)) return 0.f;  // -inf, NaN
+  if (sigmoid) return __fdiv_rn(1.f, 1.f + expf(-x));
+  // an infinite logit ties with the maximum: its exponent is 0, not inf - inf
+  return __fdiv_rn(expf(x == top ? 0.f : x - top), sum);
+}
+
+// One warp a token.  A group takes 2^lane_shift neighbouring lanes and a lane
+// PER experts in a row (the last ones of a group may be none), so that a
+// group's rank meets in a few neighbouring lanes and the order of lanes is the
+// order of experts: among equal ranks the first lane, then the first of its
+// experts wins.  An arg-max round is a maximum over the lane's keys, redux.sync
+// over the warp and a ballot; the selected experts' scores are computed again
+// from their logits, a lane each, so no scores are carried through the rounds.
+// FP32 throughout; expf and IEEE division.
 template <int TYPE, int PER>
 __global__ void __launch_bounds__(128) route_experts_kernel(const RouteArgs a) {
   pdl_wait();
@@ -41,135 +57,126 @@ __global__ void __launch_bounds__(128) route_experts_kernel(const RouteArgs a) {
   if (t >= a.T) return;
   constexpr uint32_t ALL = 0xffffffffu;
   const typename RowElem<TYPE>::T* row = static_cast<const typename RowElem<TYPE>::T*>(a.logits) + t * a.ldl;
+  const int g = lane >> a.lane_shift, in_group = (lane & ((1 << a.lane_shift) - 1)) * PER;
+  const int e0 = g * a.group_size + in_group;                                // the lane's first expert
+  const int n = g < a.groups ? min(max(a.group_size - in_group, 0), PER) : 0;  // and how many it has
 
-  float s[PER];
-  uint32_t open = 0;  // bit i: the expert exists and is not masked
+  float x[PER];
   float top = -INFINITY;
+  if (PER >= 4 && a.vec) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    s[i] = e < a.E ? RowElem<TYPE>::get(row[e]) : -INFINITY;
-    if (s[i] > -INFINITY) open |= 1u << i;  // false for NaN
-    top = fmaxf(top, s[i]);                 // ignores NaN
-  }
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = (open >> i) & 1u ? __fdiv_rn(1.f, 1.f + expf(-s[i])) : 0.f;
+    for (int i = 0; i + 3 < PER; i += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < n) v = load4<TYPE>(row, e0 + i);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
   } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, o));
-    float sum = 0.f;
+    for (int i = 0; i < PER; ++i) x[i] = i < n ? RowElem<TYPE>::get(row[e0 + i]) : -INFINITY;
+  }
+  float sum = 0.f;
+  if (!a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      // an infinite logit ties with the maximum: its exponent is 0, not inf - inf
-      s[i] = (open >> i) & 1u ? expf(s[i] == top ? 0.f : s[i] - top) : 0.f;
-      sum += s[i];
-    }
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);  // ignores NaN
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, o));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += x[i] > -INFINITY ? expf(x[i] == top ? 0.f : x[i] - top) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = sum > 0.f ? __fdiv_rn(s[i], sum) : 0.f;
   }
   uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    const float b = a.bias && e < a.E ? a.bias[e] : 0.f;
-    key[i] = e >= a.E ? KEY_NONE : (open >> i) & 1u ? rank_key(s[i] + b) : KEY_MASKED;
+    const float s = score_of(x[i], a.sigmoid, top, sum);
+    key[i] = i >= n ? KEY_NONE : x[i] > -INFINITY ? rank_key(s + (a.bias ? a.bias[e0 + i] : 0.f)) : KEY_MASKED;
   }
 
   if (a.groups > 1) {
-    // Lane g ends up with the key of group g: the sum of its best one or two
-    // unmasked ranks.
-    uint32_t gkey = KEY_NONE;
-    for (int g = 0; g < a.groups; ++g) {
-      const int lo = g * a.group_size, hi = lo + a.group_size;
-      uint32_t b1 = KEY_NONE, b2 = KEY_NONE;  // this lane's best two of the group
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        const uint32_t v = e >= lo && e < hi ? key[i] : KEY_NONE;
-        b2 = max(b2, min(b1, v));
-        b1 = max(b1, v);
-      }
-      const uint32_t m1 = __reduce_max_sync(ALL, b1);
-      uint32_t m = m1;
-      if (m1 > KEY_MASKED) {
-        float r = key_rank(m1);
-        if (a.group_top == 2) {
-          const uint32_t who = __ballot_sync(ALL, b1 == m1);
-          const uint32_t m2 = __reduce_max_sync(ALL, lane == __ffs(who) - 1 ? b2 : b1);
-          if (m2 > KEY_MASKED) r += key_rank(m2);
-        }
-        m = rank_key(r);
-      }
-      if (lane == g) gkey = m;
-    }
-    uint32_t keep = 0;
-    for (int r = 0; r < a.top_groups; ++r) {
-      const uint32_t m = __reduce_max_sync(ALL, gkey);
-      const int g = __ffs(__ballot_sync(ALL, gkey == m)) - 1;
-      keep |= 1u << g;
-      if (lane == g) gkey = KEY_NONE;
-    }
+    // the group's best two ranks, then its key in every lane of it
+    uint32_t b1 = KEY_NONE, b2 = KEY_NONE;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && !((keep >> (e / a.group_size)) & 1u)) key[i] = KEY_NONE;
+      b2 = max(b2, min(b1, key[i]));
+      b1 = max(b1, key[i]);
+    }
+    for (int o = 1; o < (1 << a.lane_shift); o <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
+      b2 = max(max(b2, o2), min(b1, o1));
+      b1 = max(b1, o1);
+    }
+    uint32_t mine = b1;
+    if (b1 > KEY_MASKED) mine = rank_key(key_rank(b1) + (a.group_top == 2 && b2 > KEY_MASKED ? key_rank(b2) : 0.f));
+    int before = 0;  // groups that come first
+    for (int h = 0; h < a.groups; ++h) {
+      const uint32_t other = __shfl_sync(ALL, mine, h << a.lane_shift);
+      before += other > mine || (other == mine && h < g);
+    }
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = KEY_NONE;
     }
   }
 
-  float my_w = 0.f;
   int my_id = 0;
-  float total = 0.f;
+#pragma unroll 1
   for (int r = 0; r < a.k; ++r) {
-    uint32_t b = KEY_NONE;
-    float bs = 0.f;
-    int be = 0x7fffffff;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (key[i] > b) {  // ascending e: ties keep the lower index
-        b = key[i];
-        bs = s[i];
-        be = lane + 32 * i;
-      }
-    const uint32_t m = __reduce_max_sync(ALL, b);
-    const int e = static_cast<int>(__reduce_min_sync(ALL, b == m ? static_cast<uint32_t>(be) : 0x7fffffffu));
-    const float we = __shfl_sync(ALL, bs, e & 31);
+    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+    const uint32_t m = __reduce_max_sync(ALL, best);
+    const int leader = __ffs(__ballot_sync(ALL, best == m)) - 1;
+    int at = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (e == lane + 32 * i) key[i] = KEY_NONE;
-    total += we;
-    if (lane == r) {
-      my_id = e;
-      my_w = we;
+    for (int i = PER - 1; i > 0; --i)
+      if (key[i] == m) at = i;
+    if (key[0] == m) at = 0;
+    const int e = __shfl_sync(ALL, e0 + at, leader);
+    if (lane == r) my_id = e;
+    if (lane == leader) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == at) key[i] = KEY_NONE;
     }
   }
+  float w = lane < a.k ? score_of(RowElem<TYPE>::get(row[my_id]), a.sigmoid, top, sum) : 0.f;
+  if (a.renorm) {
+    float total = w;  // k <= 16
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(ALL, total, o);
+    w = total > 0.f ? __fdiv_rn(w, total) : 0.f;
+  }
   if (lane < a.k) {
-    if (a.renorm) my_w = total > 0.f ? __fdiv_rn(my_w, total) : 0.f;
     a.ids[t * a.k + lane] = my_id;
-    a.w[t * a.k + lane] = my_w * a.scale;
+    a.w[t * a.k + lane] = w * a.scale;
   }
 }
 
 template <int TYPE>
-static cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
+static cudaError_t route_launch(const RouteArgs& a, int per, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.T) + 3) / 4)), block(128);
-  if (a.E <= 128) return launch_pdl(route_experts_kernel<TYPE, 4>, grid, block, 0, s, a);
-  if (a.E <= 256) return launch_pdl(route_experts_kernel<TYPE, 8>, grid, block, 0, s, a);
-  if (a.E <= 512) return launch_pdl(route_experts_kernel<TYPE, 16>, grid, block, 0, s, a);
-  return launch_pdl(route_experts_kernel<TYPE, 32>, grid, block, 0, s, a);
+  if (per <= 4) return launch_pdl(route_experts_kernel<TYPE, 4>, grid, block, 0, s, a);
+  if (per <= 8) return launch_pdl(route_experts_kernel<TYPE, 8>, grid, block, 0, s, a);
+  if (per <= 16) return launch_pdl(route_experts_kernel<TYPE, 16>, grid, block, 0, s, a);
+  if (per <= 32) return launch_pdl(route_experts_kernel<TYPE, 32>, grid, block, 0, s, a);
+  return launch_pdl(route_experts_kernel<TYPE, 64>, grid, block, 0, s, a);
 }
 
 moex_status launch_route_experts(const void* logits, int type, int64_t ldl, const float* bias, int T, int E, int k,
                                  int score, int groups, int top_groups, int group_top, int renorm, float scale,
                                  int32_t* ids, float* w, cudaStream_t s) {
-  const RouteArgs a{logits, bias,   ids,        w,         ldl,    scale,     T, E, k, score == MOEX_SCORE_SIGMOID,
-                    groups, top_groups, group_top, renorm, E / groups};
+  RouteArgs a{logits, bias,   ids,        w,         ldl,    scale,     T, k, score == MOEX_SCORE_SIGMOID,
+              groups, top_groups, group_top, renorm, E / groups};
+  // lanes a group: 32 over the groups' count rounded up to a power of two; at most 60 experts a lane (E <= 1024)
+  a.lane_shift = 5;
+  for (int g = 1; g < groups; g <<= 1) --a.lane_shift;
+  const int lanes = 1 << a.lane_shift, per = (a.group_size + lanes - 1) / lanes;
+  const uintptr_t bytes = type == MOEX_F32 ? 16 : 8;
+  a.vec = a.group_size % 4 == 0 && ldl % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % bytes == 0;
   switch (type) {
-    case MOEX_BF16: return cuda_status(route_launch<MOEX_BF16>(a, s));
-    case MOEX_F16: return cuda_status(route_launch<MOEX_F16>(a, s));
-    default: return cuda_status(route_launch<MOEX_F32>(a, s));
+    case MOEX_BF16: return cuda_status(route_launch<MOEX_BF16>(a, per, s));
+    case MOEX_F16: return cuda_status(route_launch<MOEX_F16>(a, per, s));
+    default: return cuda_status(route_launch<MOEX_F32>(a, per, s));
   }
 }
 

@@ -215,3 +215,27 @@ def test_other_stream_and_given_workspace():
         m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q, out=out, ws=ws, stream=st)
         st.synchronize()
         assert torch.equal(out, want)
+
+
+def test_binding_refusals():
+    import torch
+    m = mx()
+    p = Paged(23, [3], [40], 2, 64, 16)
+    q = _q(p, 4)
+    b = p.batch()
+    for bad in (lambda: m.paged_attention(q, p.k, p.v[:, :1], *b), lambda: m.paged_attention(q.half(), p.k, p.v, *b),
+                lambda: m.paged_attention(q, p.k, p.v, p.cu.long(), p.ctx, p.table),
+                lambda: m.paged_attention(q, p.k, p.v, p.cu[:1], p.ctx, p.table),
+                lambda: m.paged_attention(q, p.k, p.v, *b, out=torch.empty(3, 4, 65, device="cuda")),
+                lambda: m.paged_attention(q, p.k, p.v, *b, lse=torch.empty(3, 5, device="cuda")),
+                lambda: m.rope_kv_write(torch.zeros(3, 100, device="cuda"), p.k, p.v, *b, n_heads=4),
+                lambda: m.add_rms_norm(torch.zeros(2, 64, device="cuda"), torch.zeros(32, device="cuda")),
+                lambda: m.add_rms_norm(torch.zeros(2, 64, device="cuda"), torch.zeros(64, device="cuda"),
+                                       residual=torch.zeros(2, 64, device="cuda").half()),
+                lambda: m.route_experts(torch.zeros(2, 64, device="cuda"), 2, bias=torch.zeros(63, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(m.MoexError):
+        m.paged_attention(q, p.k, p.v, *b, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(m.MoexError):
+        m.paged_attention(q, p.k, p.v, *b, scale=-1.0)
