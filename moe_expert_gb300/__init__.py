@@ -5,6 +5,11 @@ kernels behind the C entry points declared in include/moex.h.  PyTorch supplies
 device memory (torch tensors) and the current CUDA stream.  There is no CPU
 fallback: if the library is missing, every call raises.
 
+The operators around a layer's products (add_rms_norm, dequantize_q8_1,
+route_experts, rope_kv_write, paged_attention) go through the extension module
+_native instead of ctypes: the same marshalling in C++, since a decode step
+makes these calls once a layer and they are short on the GPU.
+
 The function names follow the C ABI without the ``moex_`` prefix.
 """
 from __future__ import annotations
@@ -427,43 +432,23 @@ def moe_decode_noalloc(gate_up: PackedWeight, down: PackedWeight, x, ids, w, out
     return out
 
 
-_type_codes = {}
+_native_module = None
 
 
-def _type(dtype) -> int:
-    """moex_type of a torch dtype."""
-    if not _type_codes:
-        torch = _torch()
-        _type_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    code = _type_codes.get(dtype)
-    if code is None:
-        raise TypeError(f"expected float32, bfloat16 or float16, got {dtype}")
-    return code
+def _load_native():
+    """The extension module; raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        _torch()
+        from . import _native as native
+        native.set_error_class(MoexError)
+        _native_module = native
+    return _native_module
 
 
-def _rows(t, shape, what: str) -> int:
-    """Row stride of a CUDA matrix of `shape` with contiguous rows (its width
-    for a single row, whose stride says nothing)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
-    if t.shape != shape or t.stride(1) != 1:
-        raise ValueError(f"{what}: expected rows of shape {tuple(shape)}, contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1]
-
-
-def _flat(t, numel: int, dtype, what: str) -> int:
-    """Pointer of a contiguous CUDA tensor of `numel` elements of `dtype`."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
-    if t.numel() != numel or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what}: expected {numel} contiguous elements of {dtype}")
-    return t.data_ptr()
-
-
-def _float_rows(t, shape, what: str) -> int:
-    if t.dtype != _torch().float32:
-        raise ValueError(f"{what}: expected float32")
-    return _rows(t, shape, what)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def add_rms_norm(x, gamma, eps: float = 1e-6, residual=None, sum_out=None, y=None, y_dtype=None, quantize=False,
@@ -475,50 +460,14 @@ def add_rms_norm(x, gamma, eps: float = 1e-6, residual=None, sum_out=None, y=Non
     sum_out is given; it may be residual itself), y when y or y_dtype is
     given, q int8 [T, H] and ds float32 [T, H/32, 2] with quantize=True (the
     q8_1 rows that qgemv takes); None for what was not asked for."""
-    torch = _torch()
-    shape = x.shape
-    T, H = shape
-    ldx, xt = _rows(x, shape, "x"), _type(x.dtype)
-    r_ptr = s_ptr = y_ptr = q_ptr = ds_ptr = None
-    ldr = lds = ldy = yt = 0
-    if residual is not None:
-        ldr, r_ptr = _float_rows(residual, shape, "residual"), residual.data_ptr()
-        if sum_out is None:
-            sum_out = torch.empty(shape, dtype=torch.float32, device=x.device)
-    if sum_out is not None:
-        lds, s_ptr = _float_rows(sum_out, shape, "sum_out"), sum_out.data_ptr()
-    if y is None and y_dtype is not None:
-        y = torch.empty(shape, dtype=y_dtype, device=x.device)
-    if y is not None:
-        ldy, yt, y_ptr = _rows(y, shape, "y"), _type(y.dtype), y.data_ptr()
-    if quantize:
-        if q is None:
-            q = torch.empty(shape, dtype=torch.int8, device=x.device)
-        if ds is None:
-            ds = torch.empty((T, H // QK, 2), dtype=torch.float32, device=x.device)
-        q_ptr = _flat(q, T * H, torch.int8, "q")
-        ds_ptr = _flat(ds, T * (H // QK) * 2, torch.float32, "ds")
-    else:
-        q = ds = None
-    st = lib().moex_add_rms_norm(x.data_ptr(), xt, ldx, r_ptr, ldr, _flat(gamma, H, torch.float32, "gamma"), eps, T, H,
-                                 s_ptr, lds, y_ptr, yt, ldy, q_ptr, ds_ptr, _stream(stream))
-    if st:
-        _check(st, "moex_add_rms_norm")
-    return sum_out, y, q, ds
+    return (_native_module or _load_native()).add_rms_norm(x, gamma, eps, residual, sum_out, y, y_dtype, quantize, q,
+                                                           ds, _handle(stream))
 
 
 def dequantize_q8_1(q, ds, y=None, dtype=None, stream=None):
     """The values d * q of q8_1 rows (q int8 [T, K], ds [T, K/32, 2]) as
     float32 (default), bfloat16 or float16 rows."""
-    torch = _torch()
-    T, K = q.shape
-    if y is None:
-        y = torch.empty((T, K), dtype=dtype or torch.float32, device=q.device)
-    st = lib().moex_dequantize_q8_1(_flat(q, T * K, torch.int8, "q"), _flat(ds, T * (K // QK) * 2, torch.float32, "ds"),
-                                    T, K, _flat(y, T * K, y.dtype, "y"), _type(y.dtype), _stream(stream))
-    if st:
-        _check(st, "moex_dequantize_q8_1")
-    return y
+    return (_native_module or _load_native()).dequantize_q8_1(q, ds, y, dtype, _handle(stream))
 
 
 SCORE = {"softmax": 0, "sigmoid": 1}
@@ -531,56 +480,11 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
     groups (each ranked by the sum of its group_top best experts), weights =
     the selected scores, renormalised and scaled.  Returns ids int32 [T, k]
     and w float32 [T, k], as moe_decode and moe_prefill take them."""
-    torch = _torch()
-    T, E = logits.shape
     code = SCORE.get(score)
     if code is None:
         raise ValueError("score: softmax or sigmoid")
-    ldl = _rows(logits, logits.shape, "logits")
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    st = lib().moex_route_experts(logits.data_ptr(), _type(logits.dtype), ldl,
-                                  None if bias is None else _flat(bias, E, torch.float32, "bias"), T, E, k, code,
-                                  groups, top_groups, group_top, 1 if renorm else 0, scale,
-                                  _flat(ids, T * k, torch.int32, "ids"), _flat(w, T * k, torch.float32, "w"),
-                                  _stream(stream))
-    if st:
-        _check(st, "moex_route_experts")
-    return ids, w
-
-
-def _paged_kv(k_cache, v_cache) -> PagedKV:
-    if not (k_cache.is_cuda and v_cache.is_cuda):
-        raise ValueError("k_cache, v_cache: every tensor has to be a CUDA tensor")
-    n_pages, heads, page, dim = k_cache.shape
-    st = k_cache.stride()
-    if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.stride() != st or st[3] != 1):
-        raise ValueError("k_cache and v_cache: the same type, shape [pages, heads, page, dim] and strides, dim contiguous")
-    return PagedKV(_type(k_cache.dtype), page, heads, dim, n_pages, st[0], st[1], st[2], k_cache.data_ptr(),
-                   v_cache.data_ptr())
-
-
-def _batch(cu_q, ctx_len, page_table, n_tokens, max_q) -> Batch:
-    i32 = _torch().int32
-    n, width = page_table.shape
-    if not page_table.is_cuda:
-        raise ValueError("page_table: every tensor has to be a CUDA tensor")
-    if page_table.dtype != i32 or page_table.stride(1) != 1:
-        raise ValueError("page_table: expected int32 [B, width], rows contiguous")
-    return Batch(n, n_tokens, n_tokens if max_q is None else max_q, width, page_table.stride(0) if n > 1 else width,
-                 _flat(cu_q, n + 1, i32, "cu_q"), _flat(ctx_len, n, i32, "ctx_len"), page_table.data_ptr())
-
-
-def _heads(t, T: int, heads: int, dim: int, what: str) -> int:
-    """Token stride of a CUDA tensor [T, heads, dim] whose tokens are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: every tensor has to be a CUDA tensor")
-    st = t.stride()
-    if t.shape != (T, heads, dim) or st[2] != 1 or (st[1] != dim and heads > 1):
-        raise ValueError(f"{what}: expected [{T}, {heads}, {dim}], heads contiguous")
-    return st[0] if T > 1 else heads * dim
+    return (_native_module or _load_native()).route_experts(logits, k, code, bias, groups, top_groups, group_top,
+                                                            renorm, scale, ids, w, _handle(stream))
 
 
 def rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, n_heads: int, cos_sin=None,
@@ -594,34 +498,15 @@ def rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table, n_heads: int
 
     Sequence b has new tokens cu_q[b] .. cu_q[b+1]-1 and ctx_len[b] tokens in
     the cache, the new ones last; page_table [B, width] (all int32)."""
-    torch = _torch()
-    T = qkv.shape[0]
-    kv = _paged_kv(k_cache, v_cache)
-    b = _batch(cu_q, ctx_len, page_table, T, None)
-    heads, dim = kv.n_kv_heads, kv.head_dim
-    ld = _rows(qkv, (T, (n_heads + 2 * heads) * dim), "qkv")
-    rot = n_pos = 0
-    cs_ptr = None
-    if cos_sin is not None:
-        n_pos, rot = cos_sin.shape
-        cs_ptr = _flat(cos_sin, n_pos * rot, torch.float32, "cos_sin")
-    if q is None:
-        q = torch.empty((T, n_heads, dim), dtype=k_cache.dtype, device=qkv.device)
-    if q.dtype != k_cache.dtype:
-        raise ValueError("q: expected the cache's type")
-    st = lib().moex_rope_kv_write(qkv.data_ptr(), _type(qkv.dtype), ld, kv, b, n_heads, cs_ptr, n_pos, rot,
-                                  1 if interleaved else 0, q.data_ptr(), _heads(q, T, n_heads, dim, "q"),
-                                  _stream(stream))
-    if st:
-        _check(st, "moex_rope_kv_write")
-    return q
+    return (_native_module or _load_native()).rope_kv_write(qkv, k_cache, v_cache, cu_q, ctx_len, page_table,
+                                                            n_heads, cos_sin, interleaved, q, _handle(stream))
 
 
 def paged_attention_workspace_bytes(k_cache, v_cache, cu_q, ctx_len, page_table, n_tokens: int, n_heads: int,
                                     max_q: Optional[int] = None) -> int:
-    kv = _paged_kv(k_cache, v_cache)
-    b = _batch(cu_q, ctx_len, page_table, n_tokens, max_q)
-    return int(lib().moex_paged_attention_workspace_bytes(kv, b, n_heads))
+    """Bytes of the workspace that paged_attention takes for such a batch."""
+    return (_native_module or _load_native()).paged_attention_workspace_bytes(k_cache, v_cache, cu_q, ctx_len,
+                                                                              page_table, n_tokens, n_heads, max_q)
 
 
 def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optional[int] = None,
@@ -633,32 +518,9 @@ def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optio
     (None: T); it picks the kernel.  scale: 1/sqrt(dim) unless given; window >
     0: only the last `window` keys.  Returns out [T, n_heads, dim] of q's type,
     or float32 with out_dtype; lse (float32 [T, n_heads]) is filled when given."""
-    torch = _torch()
-    T, n_heads, dim = q.shape
-    kv = _paged_kv(k_cache, v_cache)
-    b = _batch(cu_q, ctx_len, page_table, T, max_q)
-    if q.dtype != k_cache.dtype or dim != kv.head_dim:
-        raise ValueError("q: expected the cache's type and head size")
-    ldq = _heads(q, T, n_heads, dim, "q")
-    if out is None:
-        out = torch.empty((T, n_heads, dim), dtype=out_dtype or q.dtype, device=q.device)
-    ldo = _heads(out, T, n_heads, dim, "out")
-    L = lib()
-    if ws is None:
-        nbytes = L.moex_paged_attention_workspace_bytes(kv, b, n_heads)
-        if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    ws_ptr, nbytes = None, 0
-    if ws is not None:
-        nbytes = ws.numel()
-        ws_ptr = _flat(ws, nbytes, torch.uint8, "ws")
-    st = L.moex_paged_attention(q.data_ptr(), ldq, kv, b, n_heads, dim ** -0.5 if scale is None else scale, window,
-                                out.data_ptr(), _type(out.dtype), ldo,
-                                None if lse is None else _flat(lse, T * n_heads, torch.float32, "lse"), ws_ptr, nbytes,
-                                _stream(stream))
-    if st:
-        _check(st, "moex_paged_attention")
-    return out
+    return (_native_module or _load_native()).paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q,
+                                                              scale, window, out, out_dtype, lse, ws,
+                                                              _handle(stream))
 
 
 def device_status(stream=None) -> int:
