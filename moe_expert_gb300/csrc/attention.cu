@@ -33,7 +33,10 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
   // with fewer units than CTAs a range is one unit or none
   const bool sparse = x.W < n_cta;
   const int parts = sparse ? x.units : static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta)) - c0 + 1;
-  const int nr = min(R, x.rows - r0), row = threadIdx.x % R;  // and columns 4 (threadIdx.x / R)
+  const int nr = min(R, x.rows - r0);
+  // thread: columns 4 (threadIdx.x / R) of one row, of every `ways`-th partial when the rows are few
+  const int shift = nr > 8 ? 4 : nr > 4 ? 3 : nr > 2 ? 2 : nr - 1, ways = R >> shift;
+  const int row = threadIdx.x & ((1 << shift) - 1), way = (threadIdx.x % R) >> shift;
   const float* stats = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
   const float* part = a.part + part_offset<MT, D>(0, r0 + row, 4 * (threadIdx.x / R));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
       const float old = rescale[row];
       acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
 #pragma unroll 4
-      for (int f = 0; f < nf; ++f) {
+      for (int f = way; f < nf; f += ways) {
         const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(slots[f]) * MT * D);
         const float wt = weight[f][row];
         acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
@@ -82,13 +85,17 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
     __syncthreads();
   }
   // by way of shared memory, so that a row is written in one piece
-  rows[row][threadIdx.x / R] = acc;
+  rows[threadIdx.x % R][threadIdx.x / R] = acc;  // row + way << shift
   __syncthreads();
   const int r = threadIdx.x / V, c = threadIdx.x % V;
   if (r >= nr) return;
   const SeqView s{x.first, x.n, x.ctx, false};
   const float l = total[r], inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
   float4 v = rows[r][c];
+  for (int y = 1; y < ways; ++y) {
+    const float4 o = rows[r + (y << shift)][c];
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
   v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
   store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r0 + r, a.ldo, D) + 4 * c, v);
   if (a.lse && c == 0)

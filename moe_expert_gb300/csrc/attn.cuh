@@ -122,94 +122,122 @@ struct Cursor {
   Tile x;
 };
 
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+  const int lane = threadIdx.x & 31;
+  if (__any_sync(0xffffffffu, v >> 25)) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  }
+  int x = static_cast<int>(v);  // 32 of these fit 32 bits
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Units of each lane's sequence and one key head; one of many tiles is counted by the whole warp.
+template <int MT, int UK, int DEAD>
+__device__ __forceinline__ int64_t lane_units(const AttnArgs& a, const SeqView& s) {
+  const bool few = s.n * a.group.n <= FEW_TILES * MT;
+  int64_t v = few ? seq_units_few<MT, UK, DEAD>(s, a.group, a.window) : 0;
+#pragma unroll 1
+  for (uint32_t many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
+    const int src = __ffs(many) - 1;
+    const SeqView w{0, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.ctx, src), false};
+    const int64_t u = seq_units_warp<MT, UK, DEAD>(w, a.group, a.window);
+    if ((threadIdx.x & 31) == src) v = u;
+  }
+  return v;
+}
+
 // Every CTA finds the batch's number of units and its own range: a scan over
 // the sequences, THREADS at a time.  The cursor is at the range's first unit,
 // and so is the CTA's entry of the plan.
 template <int MT, int UK, int DEAD, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
-  __shared__ int64_t warp_sum[2][THREADS / 32];
-  __shared__ int64_t found[2];  // units before the sequence, its units
-  __shared__ SeqView found_s;
-  __shared__ int found_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t total = 0, mine = 0, before = 0;
-  SeqView s{0, 0, 0, false};
-  // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
+  int64_t total, u0, before, units;  // of the batch; the range's first; before and in its sequence
+  if (a.b.n_seqs <= 32) {
+    // every warp for itself, a lane a sequence
+    SeqView s{0, 0, 0, false};
+    if (lane < a.b.n_seqs) s = seq_view(a.b, lane);
+    if (s.bad && threadIdx.x < 32 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+    const int64_t mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s), sum = warp_scan(mine);
+    total = __shfl_sync(0xffffffffu, sum, 31);
+    u0 = range_begin(cta, total, n_cta);
+    const uint32_t past = __ballot_sync(0xffffffffu, sum > u0);
+    const int src = past ? __ffs(past) - 1 : 0;
+    units = __shfl_sync(0xffffffffu, mine, src);
+    before = __shfl_sync(0xffffffffu, sum, src) - units;
+    cur.b = src;
+    cur.s = SeqView{__shfl_sync(0xffffffffu, s.first, src), __shfl_sync(0xffffffffu, s.n, src),
+                    __shfl_sync(0xffffffffu, s.ctx, src), false};
+  } else {
+    __shared__ int64_t warp_sum[2][THREADS / 32];
+    __shared__ int64_t found[2];  // units before the sequence, its units
+    __shared__ SeqView found_s;
+    __shared__ int found_b;
+    int64_t mine = 0, first = 0;
+    SeqView s{0, 0, 0, false};
+    total = 0;
+    // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
-    int64_t run = 0;
-    for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
-      const int b = base + threadIdx.x;
-      if (pass == 0 || a.b.n_seqs > THREADS) {
-        // a thread a sequence; one of many tiles is counted by the whole warp
-        s = SeqView{0, 0, 0, false};
-        if (b < a.b.n_seqs) s = seq_view(a.b, b);
-        if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-        const bool few = s.n * a.group.n <= FEW_TILES * MT;
-        int64_t v = few ? seq_units_few<MT, UK, DEAD>(s, a.group, a.window) : 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
+      int64_t run = 0;
 #pragma unroll 1
-        for (uint32_t many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
-          const int src = __ffs(many) - 1;
-          SeqView w{0, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.ctx, src), false};
-          const int64_t u = seq_units_warp<MT, UK, DEAD>(w, a.group, a.window);
-          if (lane == src) v = u;
-        }
-        v *= a.n_kv_heads;
-        mine = v;
-        // sums over the warps that have sequences
-        const int warps = min((a.b.n_seqs - base + 31) / 32, THREADS / 32);
-        int64_t x = v;
-        if (warp < warps) {
-          if (__any_sync(0xffffffffu, v >> 25)) {
-#pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-              const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-              if (lane >= o) x += y;
-            }
-          } else {  // the warp's sum fits 32 bits
-            int x32 = static_cast<int>(v);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int y = __shfl_up_sync(0xffffffffu, x32, o);
-              if (lane >= o) x32 += y;
-            }
-            x = x32;
-          }
+      for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
+        const int b = base + threadIdx.x;
+        if (pass == 0 || a.b.n_seqs > THREADS) {
+          s = SeqView{0, 0, 0, false};
+          if (b < a.b.n_seqs) s = seq_view(a.b, b);
+          if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+          mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s);
+          const int64_t x = warp_scan(mine);
           if (lane == 31) warp_sum[it & 1][warp] = x;
+          __syncthreads();
+          const int warps = min((a.b.n_seqs - base + 31) / 32, THREADS / 32);
+          first = run;
+          for (int w = 0; w < warps; ++w) {
+            const int64_t ws = warp_sum[it & 1][w];
+            if (w < warp) first += ws;
+            run += ws;
+          }
+          first += x - mine;
         }
+        if (pass == 1 && mine > 0 && first <= want && want < first + mine) {
+          found_b = b;
+          found_s = s;
+          found[0] = first;
+          found[1] = mine;
+        }
+      }
+      if (pass == 0)
+        total = run;
+      else
         __syncthreads();
-        before = run;
-        for (int w = 0; w < warps; ++w) {
-          const int64_t ws = warp_sum[it & 1][w];
-          if (w < warp) before += ws;
-          run += ws;
-        }
-        before += x - v;
-      }
-      if (pass == 1 && mine > 0 && before <= want && want < before + mine) {
-        found_b = b;
-        found_s = s;
-        found[0] = before;
-        found[1] = mine;
-      }
     }
-    if (pass == 0)
-      total = run;
-    else
-      __syncthreads();
+    u0 = range_begin(cta, total, n_cta);
+    before = found[0];
+    units = found[1];
+    cur.b = found_b;
+    cur.s = found_s;
   }
-  const int64_t u0 = range_begin(cta, total, n_cta);
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
   if (cur.left == 0) {
     if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
-  cur.b = found_b;
-  cur.s = found_s;
-  int64_t off = u0 - found[0];
-  const int64_t per = found[1] >> 32 ? found[1] / a.n_kv_heads
-                                     : static_cast<uint32_t>(found[1]) / static_cast<uint32_t>(a.n_kv_heads);
+  int64_t off = u0 - before;
+  const int64_t per =
+      units >> 32 ? units / a.n_kv_heads : static_cast<uint32_t>(units) / static_cast<uint32_t>(a.n_kv_heads);
   cur.hk = static_cast<int>((off | per) >> 32 ? off / per : static_cast<uint32_t>(off) / static_cast<uint32_t>(per));
   off -= cur.hk * per;
   cur.t = 0;
@@ -218,12 +246,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   for (int t0 = 0; cur.s.n * a.group.n > MT; t0 += 32) {
     const int t = t0 + lane;
     const int n = t * MT < cur.s.n * a.group.n ? tile_of<MT, UK>(cur.s, a.group, a.window, t).units + DEAD : 0;
-    int64_t sum = n;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
+    const int64_t sum = warp_scan(n);
     const uint32_t past = __ballot_sync(0xffffffffu, sum > off);
     if (past) {
       const int src = __ffs(past) - 1;
