@@ -98,7 +98,8 @@ __device__ __forceinline__ int64_t seq_units_warp(const SeqView& s, const HeadGr
   const int tiles = (s.n * group.n + MT - 1) / MT;
   int64_t u = 0;
   for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_of<MT, UK>(s, group, window, t).units + DEAD;
-#pragma unroll
+  if (!__any_sync(0xffffffffu, u >> 25)) return __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(u));
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   return u;
 }
@@ -157,18 +158,19 @@ __device__ __forceinline__ int64_t lane_units(const AttnArgs& a, const SeqView& 
   return v;
 }
 
-// Every CTA finds the batch's number of units and its own range: a scan over
-// the sequences, THREADS at a time.  The cursor is at the range's first unit,
-// and so is the CTA's entry of the plan.
+// Every CTA finds the batch's number of units and its own range; the cursor is
+// at the range's first unit, and so is the CTA's entry of the plan.  For up to
+// WARP_SEQS sequences a warp needs no other, a lane a sequence, and a kernel may
+// leave it to one warp; for more, all threads of the CTA have to call it.
+constexpr int WARP_SEQS = 32;
 template <int MT, int UK, int DEAD, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total, u0, before, units;  // of the batch; the range's first; before and in its sequence
-  if (a.b.n_seqs <= 32) {
-    // every warp for itself, a lane a sequence
+  if (a.b.n_seqs <= WARP_SEQS) {
     SeqView s{0, 0, 0, false};
     if (lane < a.b.n_seqs) s = seq_view(a.b, lane);
-    if (s.bad && threadIdx.x < 32 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+    if (s.bad && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
     const int64_t mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s), sum = warp_scan(mine);
     total = __shfl_sync(0xffffffffu, sum, 31);
     u0 = range_begin(cta, total, n_cta);
@@ -232,7 +234,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   }
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
   if (cur.left == 0) {
-    if (threadIdx.x == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (lane == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   int64_t off = u0 - before;
@@ -261,7 +263,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   off -= DEAD;
   if (off < 0) cur.left += off;  // the range begins among the tile's dead units
   cur.u = static_cast<int>(max(off, int64_t(0)));
-  if (threadIdx.x == 0)
+  if (lane == 0)  // of every warp that is here: the same values
     a.plan[cta] = RangeStart{total, tile_u, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0,
                              cur.s.first, cur.s.n, cur.s.ctx, 0};
 }

@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
   }
   pdl_wait();
   Cursor& cur = cursors[warp];
-  {
+  if (a.b.n_seqs > WARP_SEQS || warp == 0) {
     Cursor at;
     find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at);
-    if (lane == 0) cur = at;
+    if (warp == 0 && lane < THREADS / 32) cursors[lane] = at;
   }
   tc_fence_before();
   __syncthreads();

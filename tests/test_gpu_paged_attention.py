@@ -139,6 +139,18 @@ def test_growing_scores():
         _check(p, 2, q=q)
 
 
+@pytest.mark.parametrize("B", [33, 150, 700])
+@pytest.mark.parametrize("hint", [None, 200])
+def test_many_sequences(B, hint):
+    """More sequences than a warp, a CTA of either kernel, has lanes."""
+    g = np.random.Generator(np.random.PCG64(B))
+    n = g.integers(0, 4, B)
+    n[B // 2] = 60
+    total = n + g.integers(0, 70, B)
+    p = Paged(B, n.tolist(), total.tolist(), 2, 64, 16)
+    _check(p, 4, max_q=min(hint or 1, p.T))
+
+
 def test_wrong_hint_costs_time_only():
     import torch
     m = mx()
