@@ -6,8 +6,8 @@
 
 namespace moex {
 
-// Tiles that ranges cut, one column of CTAs for each range that begins inside a
-// tile and is the first to do so, a CTA for 16 rows: the partials in the order of
+// Tiles that ranges cut, a CTA for each range that begins inside a
+// tile of at most 16 rows and is the first to do so: the partials in the order of
 // their keys, FP32.  CTA c of the first kernel leaves its first tile in slot 2c
 // when it begins inside it, and its last in slot 2c + 1 when it does not finish
 // it.  Latency bounds this kernel, so the rows' weights of up to 32 partials are
@@ -21,24 +21,24 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
   __shared__ int slots[F];
   __shared__ float rescale[R], total[R], top[R];
   __shared__ float4 rows[R][V + 1];
-  const int n_cta = gridDim.x, r0 = blockIdx.y * R;
+  const int n_cta = gridDim.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   const RangeStart x = a.plan[blockIdx.x];
-  if (x.u == 0 || r0 >= x.rows) return;  // begins with a tile, or has no units
+  if (x.u == 0) return;  // begins with a tile, or has no units
   const int64_t u0 = x.tile_u + x.u;
   if (range_begin(range_of(u0 - 1, x.W, n_cta), x.W, n_cta) > x.tile_u) return;  // an earlier range cut it first
   const int c0 = static_cast<int>(range_of(x.tile_u, x.W, n_cta));
   // with fewer units than CTAs a range is one unit or none
   const bool sparse = x.W < n_cta;
   const int parts = sparse ? x.units : static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta)) - c0 + 1;
-  const int nr = min(R, x.rows - r0);
+  const int nr = min(R, x.rows);
   // thread: columns 4 (threadIdx.x / R) of one row, of every `ways`-th partial when the rows are few
   const int shift = nr > 8 ? 4 : nr > 4 ? 3 : nr > 2 ? 2 : nr - 1, ways = R >> shift;
   const int row = threadIdx.x & ((1 << shift) - 1), way = (threadIdx.x % R) >> shift;
   const float* stats = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
-  const float* part = a.part + part_offset<MT, D>(0, r0 + row, 4 * (threadIdx.x / R));
+  const float* part = a.part + part_offset<MT, D>(0, row, 4 * (threadIdx.x / R));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int f0 = 0; f0 < parts; f0 += F) {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
     for (int r = warp; r < nr; r += WARPS) {
       float2 p = make_float2(-INFINITY, 0.f);
       if (lane < nf)
-        p = *reinterpret_cast<const float2*>(stats + 2 * (static_cast<int64_t>(slots[lane]) * MT + r0 + r));
+        p = *reinterpret_cast<const float2*>(stats + 2 * (static_cast<int64_t>(slots[lane]) * MT + r));
       const float old = f0 ? top[r] : -INFINITY;
       float m = fmaxf(old, p.x);
 #pragma unroll
@@ -97,10 +97,78 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
   }
   v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-  store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r0 + r, a.ldo, D) + 4 * c, v);
+  store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r, a.ldo, D) + 4 * c, v);
   if (a.lse && c == 0)
-    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r0 + r, a.n_heads, 1)] =
+    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] =
         l > 0.f ? top[r] * LN2 + logf(l) : -INFINITY;
+}
+
+// The same for tiles of many rows, which few ranges cut: a thread has 16 columns
+// of a row, and reads two partials of them, with their statistics, at a time.  blockIdx.y: 32 rows.
+template <int CT, int D, int MT>
+__global__ void __launch_bounds__(2 * D) attend_join_rows_kernel(const AttnArgs a) {
+  const int n_cta = gridDim.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const RangeStart x = a.plan[blockIdx.x];
+  const int r = blockIdx.y * 32 + threadIdx.x % 32, c0 = 16 * (threadIdx.x / 32);
+  if (x.u == 0 || r >= x.rows) return;  // begins with a tile, or has no units
+  const int64_t u0 = x.tile_u + x.u;
+  if (range_begin(range_of(u0 - 1, x.W, n_cta), x.W, n_cta) > x.tile_u) return;  // an earlier range cut it first
+  const int first = static_cast<int>(range_of(x.tile_u, x.W, n_cta));
+  const bool sparse = x.W < n_cta;  // a range is one unit or none
+  const int parts = sparse ? x.units : static_cast<int>(range_of(x.tile_u + x.units - 1, x.W, n_cta)) - first + 1;
+  const float* stats = a.part + static_cast<int64_t>(2 * n_cta) * MT * D;
+  float acc[16], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int f0 = 0; f0 < parts; f0 += 2) {
+    float2 ml[2];
+    float4 v[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int f = f0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (f < parts) {
+        const int c = sparse ? static_cast<int>(range_of(x.tile_u + f, x.W, n_cta)) : first + f;
+        const int64_t slot = 2 * static_cast<int64_t>(c) + (f == 0 ? 1 : 0);
+        ml[k] = *reinterpret_cast<const float2*>(stats + 2 * (slot * MT + r));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[k][j] = *reinterpret_cast<const float4*>(a.part + part_offset<MT, D>(slot, r, c0 + 4 * j));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    const float mn = fmaxf(m, fmaxf(ml[0].x, ml[1].x)), ref = mn == -INFINITY ? 0.f : mn;
+    const float k0 = fast_exp2(m - ref), w0 = fast_exp2(ml[0].x - ref), w1 = fast_exp2(ml[1].x - ref);
+    m = mn;
+    l = l * k0 + w0 * ml[0].y + w1 * ml[1].y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[4 * j] = acc[4 * j] * k0 + w0 * v[0][j].x + w1 * v[1][j].x;
+      acc[4 * j + 1] = acc[4 * j + 1] * k0 + w0 * v[0][j].y + w1 * v[1][j].y;
+      acc[4 * j + 2] = acc[4 * j + 2] * k0 + w0 * v[0][j].z + w1 * v[1][j].z;
+      acc[4 * j + 3] = acc[4 * j + 3] * k0 + w0 * v[0][j].w + w1 * v[1][j].w;
+    }
+  }
+  const SeqView s{x.first, x.n, x.ctx, false};
+  const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+  const int64_t off = row_offset(s, a.group, x.hk, x.t * MT + r, a.ldo, D) + c0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = acc[8 * h + i] * inv;
+    if (a.out_f32)
+      store8<MOEX_F32>(a.out, off + 8 * h, o);
+    else
+      store8<CT>(a.out, off + 8 * h, o);
+  }
+  if (a.lse && c0 == 0)
+    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
 }
 
 namespace {
@@ -130,9 +198,9 @@ HeadGroup head_group(int n, int n_tokens) {
 
 template <int CT, int D>
 cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
-  const dim3 grid(g.ctas, g.mt / JOIN_ROWS), block(JOIN_ROWS * D / 4);
-  return g.tile ? launch_pdl(attend_join_kernel<CT, D, TILE_MT>, grid, block, 0, s, a)
-                : launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, grid, block, 0, s, a);
+  if (g.tile)
+    return launch_pdl(attend_join_rows_kernel<CT, D, TILE_MT>, dim3(g.ctas, TILE_MT / 32), dim3(2 * D), 0, s, a);
+  return launch_pdl(attend_join_kernel<CT, D, STREAM_MT>, dim3(g.ctas), dim3(JOIN_ROWS * D / 4), 0, s, a);
 }
 
 }  // namespace
