@@ -66,7 +66,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // One tile of a sequence's rows and the keys that its rows see.
 struct Tile {
   int r0, r1;  // rows
-  int lo, hi;  // keys [lo, hi); lo is a multiple of 16
+  int lo, hi;  // keys [lo, hi)
   int units;   // at least one, so that rows without keys are written too
 };
 
@@ -77,8 +77,11 @@ __device__ __forceinline__ Tile tile_of(const SeqView& s, const HeadGroup& group
   x.r1 = min(s.n * group.n, x.r0 + MT);
   const int base = s.ctx - s.n;
   x.hi = max(base + group.token(x.r1 - 1) + 1, 0);
-  x.lo = window > 0 ? max(base + group.token(x.r0) - window + 1, 0) & ~15 : 0;
-  x.lo = min(x.lo, x.hi & ~15);
+  // whole runs of eight keys for the copies; in the kernel of large tiles whole blocks, so that a block
+  // begins where a box of the cache does
+  constexpr int ALIGN = MT >= 128 ? UK : 16;
+  x.lo = window > 0 ? max(base + group.token(x.r0) - window + 1, 0) & ~(ALIGN - 1) : 0;
+  x.lo = min(x.lo, x.hi & ~(ALIGN - 1));
   x.units = max((x.hi - x.lo + UK - 1) / UK, 1);
   return x;
 }
@@ -163,8 +166,16 @@ __device__ __forceinline__ int64_t lane_units(const AttnArgs& a, const SeqView& 
 // WARP_SEQS sequences a warp needs no other, a lane a sequence, and a kernel may
 // leave it to one warp; for more, all threads of the CTA have to call it.
 constexpr int WARP_SEQS = 32;
+template <int THREADS>
+struct RangeScratch {  // in shared memory, used before the function returns only
+  int64_t warp_sum[2][THREADS / 32];
+  int64_t before, units;
+  SeqView s;
+  int b;
+};
 template <int MT, int UK, int DEAD, int THREADS>
-__device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur) {
+__device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur,
+                                           RangeScratch<THREADS>& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total, u0, before, units;  // of the batch; the range's first; before and in its sequence
   if (a.b.n_seqs <= WARP_SEQS) {
@@ -182,10 +193,6 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
     cur.s = SeqView{__shfl_sync(0xffffffffu, s.first, src), __shfl_sync(0xffffffffu, s.n, src),
                     __shfl_sync(0xffffffffu, s.ctx, src), false};
   } else {
-    __shared__ int64_t warp_sum[2][THREADS / 32];
-    __shared__ int64_t found[2];  // units before the sequence, its units
-    __shared__ SeqView found_s;
-    __shared__ int found_b;
     int64_t mine = 0, first = 0;
     SeqView s{0, 0, 0, false};
     total = 0;
@@ -203,22 +210,22 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
           if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
           mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s);
           const int64_t x = warp_scan(mine);
-          if (lane == 31) warp_sum[it & 1][warp] = x;
+          if (lane == 31) sh.warp_sum[it & 1][warp] = x;
           __syncthreads();
           const int warps = min((a.b.n_seqs - base + 31) / 32, THREADS / 32);
           first = run;
           for (int w = 0; w < warps; ++w) {
-            const int64_t ws = warp_sum[it & 1][w];
+            const int64_t ws = sh.warp_sum[it & 1][w];
             if (w < warp) first += ws;
             run += ws;
           }
           first += x - mine;
         }
         if (pass == 1 && mine > 0 && first <= want && want < first + mine) {
-          found_b = b;
-          found_s = s;
-          found[0] = first;
-          found[1] = mine;
+          sh.b = b;
+          sh.s = s;
+          sh.before = first;
+          sh.units = mine;
         }
       }
       if (pass == 0)
@@ -227,10 +234,10 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         __syncthreads();
     }
     u0 = range_begin(cta, total, n_cta);
-    before = found[0];
-    units = found[1];
-    cur.b = found_b;
-    cur.s = found_s;
+    before = sh.before;
+    units = sh.units;
+    cur.b = sh.b;
+    cur.s = sh.s;
   }
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
   if (cur.left == 0) {

@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   pdl_wait();
   pdl_launch_dependents();  // the joining kernel's CTAs fit beside these, and wait
   Cursor cur;
-  find_range<MT, UK, DEAD, WARPS * 32>(a, blockIdx.x, gridDim.x, cur);
+  __shared__ RangeScratch<WARPS * 32> scratch;
+  find_range<MT, UK, DEAD, WARPS * 32>(a, blockIdx.x, gridDim.x, cur, scratch);
   if (cur.left <= 0) return;
   const uint32_t ring = smem_u32(sm) + warp * STAGES * 2 * S::PLANE;
 

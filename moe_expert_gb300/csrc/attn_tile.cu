@@ -7,10 +7,14 @@
 //   - O of a group: 128 x D FP32 in TMEM.  4 * 128 columns hold both groups.
 // Both groups use one copy of every key block: 64 KB of cache feed 4 products of
 // 128 x 128 x 128.
-// Warps: 0-3 copy keys and values (cp.async: pages may be as short as eight
-// keys, which as TMA boxes would be 2 KB each and bound by the box rate),
-// 4-7 and 8-11 the softmax of the two groups, one row a thread, so maxima and
-// sums need no exchange; 12 issues the MMAs; 13-15 copy Q.
+// Warps: 0 issues the MMAs; 1-3 copy keys, values and queries; 4-7 and 8-11 are
+// the softmax of the two groups, one row a thread, so maxima and sums need no
+// exchange (192 registers: a row's 128 scores stay in them).  A block of keys
+// comes by TMA, a box for each page and 64 features (the issuing lanes take no
+// time from the softmax, which cp.async address arithmetic did: 398 -> 345 us for
+// 2048 tokens over 14336 keys with 32 heads); a block that the sequence does not
+// fill, or that has a page out of range, comes by cp.async with zeros in place of
+// what is not there, since a value beside a probability of 0 must be finite.
 // The MMA order is PV0(j), QK0(j+1), PV1(j), QK1(j+1): while one group's
 // products run the other's softmax does.  A row's reference for the exponentials
 // follows its maximum only when that grows by more than 2^8, so O is rescaled
@@ -24,7 +28,8 @@ namespace moex {
 namespace {
 
 constexpr int MT = TILE_MT, UK = TILE_UK, DEAD = TILE_DEAD;
-constexpr int THREADS = 512;
+constexpr int TILE_BOX = 64;  // slots of a TMA box at most
+constexpr int THREADS = 384, LOADERS = 3, SOFTMAX0 = 4;  // warps 1-3 copy, 4-11 softmax
 constexpr float GROW = 8.f;  // log2 of the growth of a maximum that rescales O
 
 template <int D>
@@ -35,8 +40,10 @@ struct Lay {
   static constexpr int Q = 0;                         // [group][half]
   static constexpr int RING = 2 * STAGE;
   static constexpr int BARS = RING + NS * STAGE;
-  static constexpr int N_BARS = 2 * NS + 2 + 8 + 1;
-  static constexpr int BYTES = BARS + N_BARS * 8 + 16;
+  static constexpr int N_BARS = 2 * NS + 2 + 10 + 1;
+  static constexpr int CURSORS = BARS + N_BARS * 8;
+  static constexpr int FLAGS = CURSORS + (SOFTMAX0 + 2) * sizeof(Cursor);  // TMEM address, abort flag
+  static constexpr int BYTES = FLAGS + 8;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -166,16 +173,19 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 template <int CT, int D>
-__global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(THREADS, 1)
+    attend_tile_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const int tma) {
   extern __shared__ __align__(1024) uint8_t sm[];
   using L = Lay<D>;
   using E = RowElem<CT>;
   constexpr int CH = D / 8;  // 16-byte chunks of a row
   constexpr int NS = L::NS;
-  __shared__ uint32_t tmem_holder;
-  __shared__ int abort_word;
-  __shared__ Cursor cursors[THREADS / 32];  // every warp walks the range by itself; not kept in its registers
-  volatile int* abort_flag = &abort_word;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::FLAGS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::FLAGS + 4);
+  // The range is walked by the MMA warp, by each copying warp, and by each softmax
+  // group together; the cursors stay out of the registers.
+  Cursor* cursors = reinterpret_cast<Cursor*>(sm + L::CURSORS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + L::BARS);
   uint64_t* kv_empty = kv_full + NS;
@@ -185,40 +195,43 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* o_empty = o_full + 2;
-  uint64_t* done = o_empty + 2;
+  uint64_t* meet = o_empty + 2;  // the warps of a softmax group
+  uint64_t* done = meet + 2;
 
   if (threadIdx.x == 0) {
-    abort_word = 0;
+    *abort_flag = 0;
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&kv_full[i], 4);   // the four copying warps
+      mbar_init(&kv_full[i], LOADERS);
       mbar_init(&kv_empty[i], 1);  // a commit
     }
-    mbar_init(q_full, 3);
+    mbar_init(q_full, LOADERS);
     mbar_init(q_empty, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
       mbar_init(&o_full[g], 1);
       mbar_init(&o_empty[g], 4);
+      mbar_init(&meet[g], 4);
     }
     mbar_init(done, 1);
     fence_mbar_init();
   }
-  if (warp == 12) {
-    tmem_alloc(&tmem_holder, 512);
+  if (warp == SOFTMAX0) {
+    tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   pdl_wait();
-  Cursor& cur = cursors[warp];
+  Cursor& cur = cursors[warp < SOFTMAX0 ? warp : SOFTMAX0 + (warp - SOFTMAX0) / 4];
   if (a.b.n_seqs > WARP_SEQS || warp == 0) {
     Cursor at;
-    find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at);
-    if (warp == 0 && lane < THREADS / 32) cursors[lane] = at;
+    find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at,
+                                      *reinterpret_cast<RangeScratch<THREADS>*>(sm + L::Q));  // not in use yet
+    if (warp == 0 && lane < SOFTMAX0 + 2) cursors[lane] = at;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_holder;
+  const uint32_t tmem = *tmem_holder;
   const uint32_t smb = smem_u32(sm);
 
   // A wait of a whole warp: all of its lanes go on, or none.
@@ -234,18 +247,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
     __syncwarp();
   };
 
-  if (warp < 4) {
-    // ------------------------------------------------ keys and values
-    regs_down<80>();
-    // A warp copies 32 keys of a block: four runs of 8, each inside one page.
+  if (warp < SOFTMAX0) regs_down<120>();
+  if (tma && threadIdx.x == 32) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp >= 1 && warp < SOFTMAX0) {
+    // ------------------------------------------------ keys, values, queries
+    // A block is 16 runs of 8 keys, each inside one page; warp w copies runs
+    // w - 1, w + 2, ...
     constexpr int RPI = 32 / CH;      // rows an instruction covers: 2 or 4
     constexpr int PER_RUN = 8 / RPI;  // instructions a run takes
-    const int c = lane % CH, r0 = lane / CH;
+    constexpr int RUNS = (16 + LOADERS - 1) / LOADERS;
+    const int lw = warp - 1, c = lane % CH, r0 = lane / CH;
     uint32_t dst0[PER_RUN];
 #pragma unroll
     for (int i = 0; i < PER_RUN; ++i) {
       const int r = i * RPI + r0;
-      dst0[i] = smb + L::RING + (c >> 3) * L::HALF + (32 * warp + r) * 128 + (((c & 7) ^ r) << 4);
+      dst0[i] = (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ r) << 4);
     }
     const int64_t rows = RPI * a.b.row_stride, mine_at = r0 * a.b.row_stride + 8 * c;
     Ring<NS> ring;
@@ -260,34 +279,31 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
       }
     };
     bool ok = true;
-    while (cur.left > 0 && ok) {
+    for (int tile = 0; cur.left > 0 && ok; ++tile) {
       const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
       const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, hk = cur.hk;
       const int32_t* table = a.b.table + cur.b * a.b.table_stride;
-      // lane l < 4: the page of this warp's run l of a block, read a block ahead and looked at when its turn comes
+      // lane l < 16: the page of run l of a block, read a block ahead and looked at when its turn comes
       auto fetch_page = [&](int j) {
-        j += 32 * warp + 8 * lane;
-        return lane < 4 && j < hi ? __ldg(table + (j >> a.b.page_shift)) : -1;
+        j += 8 * lane;
+        return lane < 16 && j < hi ? __ldg(table + (j >> a.b.page_shift)) : -1;
       };
       int pg = fetch_page(first);
-      for (int i = 0; i < units && ok; ++i) {
-        const int j0 = first + i * UK, j = j0 + 32 * warp + 8 * lane;
+      for (int i = 0; i < units; ++i) {
+        const int j0 = first + i * UK, j = j0 + 8 * lane;
         // the offset of the run's first row, -1 for none
         int64_t mine = -1;
         if (pg >= 0 && pg < a.b.n_pages)
           mine = kv_offset(a.b, pg, hk, j);
-        else if (lane < 4 && j < hi)
+        else if (lane < 16 && j < hi)
           flag_status(a.b.status, DEV_BAD_BATCH);
+        const int pages = pg;  // of this block's runs
+        const bool whole = __all_sync(0xffffffffu, lane >= 16 || mine >= 0) && j0 + UK <= hi;
         if (i + 1 < units) pg = fetch_page(j0 + UK);
-        int64_t off[4];
-        bool whole = true;
+        int64_t off[RUNS];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          off[n] = __shfl_sync(0xffffffffu, mine, n);
-          whole = whole && off[n] >= 0;
-          off[n] += off[n] >= 0 ? mine_at : 0;
-        }
-        whole = whole && j0 + 32 * warp + 32 <= hi;
+        for (int n = 0; n < RUNS; ++n) off[n] = __shfl_sync(0xffffffffu, mine, (lw + LOADERS * n) & 15);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (filled && !__all_sync(0xffffffffu, mbar_test(&kv_empty[ring.slot], ring.parity ^ 1))) {
             // about to wait: hand over everything that is under way first
@@ -296,23 +312,50 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             ok = warp_wait(&kv_empty[ring.slot], ring.parity ^ 1, DEV_TIMEOUT_PIPE);
             if (!ok) break;
           }
-          const uint32_t dst = ring.slot * L::STAGE;
-          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.v : a.k);
+          const uint32_t dst = smb + L::RING + ring.slot * L::STAGE;
+          if (whole && tma) {
+            // every key of the block is there: boxes of one page, 64 features wide, a lane a box
+            if (untold) {
+              cp_wait<0>();
+              announce(0);
+            }
+            if (lw == 0) {
+              if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], L::STAGE);
+              __syncwarp();
+              const int box = min(1 << a.b.page_shift, TILE_BOX), part = lane % (D / 64), key = lane / (D / 64) * box;
+              const int page = __shfl_sync(0xffffffffu, pages, (key >> 3) & 15);
+              if (key < UK)
+                tma_load_4d(dst + part * L::HALF + key * 128, kv ? &vmap : &kmap, 64 * part,
+                            (j0 + key) & ((1 << a.b.page_shift) - 1), hk, page, &kv_full[ring.slot]);
+            } else if (lane == 0) {
+              mbar_arrive(&kv_full[ring.slot]);
+            }
+            ring.next();
+            told_slot = ring.slot;
+            filled = filled || ring.slot == 0;
+            continue;
+          }
+          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.v : a.k) + mine_at;
           if (whole) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < RUNS; ++n) {
+              const int run = lw + LOADERS * n;
               const uint16_t* p = src + off[n];
+              if (run < 16) {
 #pragma unroll
-              for (int k = 0; k < PER_RUN; ++k, p += rows) cp_async16(dst + dst0[k] + n * 1024, p, 16u);
+                for (int k = 0; k < PER_RUN; ++k) cp_async16(dst + dst0[k] + run * 1024, p + k * rows, 16u);
+              }
             }
           } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
+#pragma unroll 1
+            for (int run = lw; run < 16; run += LOADERS) {
+              const int64_t at = __shfl_sync(0xffffffffu, mine, run);
 #pragma unroll
               for (int k = 0; k < PER_RUN; ++k) {
-                const bool in = off[n] >= 0 && j0 + 32 * warp + 8 * n + k * RPI + r0 < hi;
-                cp_async16(dst + dst0[k] + n * 1024, src + (in ? off[n] + k * rows : 0), in ? 16u : 0u);
+                const bool in = at >= 0 && j0 + 8 * run + k * RPI + r0 < hi;
+                cp_async16(dst + dst0[k] + run * 1024, in ? src + at + k * rows : src - mine_at, in ? 16u : 0u);
               }
+            }
           }
           cp_commit();
           ++untold;
@@ -323,14 +366,45 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             announce(2);
           }
         }
+        if (!ok) break;
+        if (i == 0) {
+          // the tile's queries, when the previous tile's are done with
+          cp_wait<0>();
+          announce(0);
+          if (tile > 0) ok = warp_wait(q_empty, (tile - 1) & 1, DEV_TIMEOUT_PIPE);
+          if (!ok) break;
+          // 32 rows at a time: lane l finds where row l is, then the warp copies RPI rows an instruction
+          const int q_rows = cur.x.r1 - cur.x.r0;
+          for (int b0 = 32 * lw; b0 < q_rows; b0 += 32 * LOADERS) {
+            const int64_t at =
+                b0 + lane < q_rows ? row_offset(cur.s, a.group, hk, cur.x.r0 + b0 + lane, a.ldq, D) : -1;
+            const uint32_t qdst = smb + L::Q + (b0 >> 7) * L::STAGE + (c >> 3) * L::HALF + (b0 & 127) * 128;
+#pragma unroll 4
+            for (int k = 0; k < 32 / RPI; ++k) {
+              const int r = k * RPI + r0;
+              const int64_t off = __shfl_sync(0xffffffffu, at, r);
+              cp_async16(qdst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                         static_cast<const uint16_t*>(a.q) + (off >= 0 ? off + 8 * c : 0), off >= 0 ? 16u : 0u);
+            }
+          }
+          cp_commit();
+          cp_wait<0>();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
       }
       advance(units);
     }
     cp_wait<0>();
     if (ok) announce(0);
-  } else if (warp >= 12) {
-    regs_down<80>();
-    if (warp == 12) {
+    if (*abort_flag) {
+      // some wait ran out: boxes may still be under way, and nobody waits for them any more
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
+  } else if (warp == 0) {
       // ------------------------------------------------ MMA issue
       constexpr uint32_t IDESC_S = idesc_16_f32(128, 128, CT == MOEX_BF16, false);
       constexpr uint32_t IDESC_O = idesc_16_f32(128, D, CT == MOEX_BF16, true);
@@ -371,7 +445,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           const bool more = i + 1 < units;
           kr.next2();
           ok = warp_wait(&kv_full[vr.slot], vr.parity, DEV_TIMEOUT_MMA);
-          if (ok && more) ok = warp_wait(&kv_full[kr.slot], kr.parity, DEV_TIMEOUT_MMA);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (!ok || g >= groups) break;
@@ -385,10 +458,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             tc_fence_after();
             second(g, vr.slot, i > 0);
             if (g == groups - 1) mma_commit_elect(&kv_empty[vr.slot]);
-            if (more)
+            if (more) {
+              if (g == 0) {
+                ok = warp_wait(&kv_full[kr.slot], kr.parity, DEV_TIMEOUT_MMA);
+                if (!ok) break;
+                tc_fence_after();
+              }
               first(g, kr.slot);
-            else
+            } else {
               mma_commit_elect(&o_full[g]);
+            }
           }
           if (!ok) break;
           if (more) mma_commit_elect(&kv_empty[kr.slot]);
@@ -401,45 +480,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
       mma_commit_elect(done);
       mbar_wait(done, 0, nullptr);
       __syncwarp();
-    } else {
-      // ------------------------------------------------ queries
-      int tile = 0;
-      while (cur.left > 0) {
-        const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
-        if (tile > 0 && !warp_wait(q_empty, (tile - 1) & 1, DEV_TIMEOUT_PIPE)) break;
-        // 32 rows at a time: lane l finds where row l is, then the warp copies RPI rows an instruction
-        constexpr int RPI = 32 / CH;
-        const int rows = cur.x.r1 - cur.x.r0, c = lane % CH;
-        for (int r0 = 32 * (warp - 13); r0 < rows; r0 += 96) {
-          const int64_t mine = r0 + lane < rows ? row_offset(cur.s, a.group, cur.hk, cur.x.r0 + r0 + lane, a.ldq, D) : -1;
-          const uint32_t dst = smb + L::Q + (r0 >> 7) * L::STAGE + (c >> 3) * L::HALF + (r0 & 127) * 128;
-#pragma unroll 8
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int r = i * RPI + lane / CH;
-            const int64_t off = __shfl_sync(0xffffffffu, mine, r);
-            cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       static_cast<const uint16_t*>(a.q) + (off >= 0 ? off + 8 * c : 0), off >= 0 ? 16u : 0u);
-          }
-        }
-        cp_commit();
-        cp_wait<0>();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        ++tile;
-        advance(units);
-      }
-    }
   } else {
     // ------------------------------------------------ softmax
-    regs_up<176>();
-    const int g = (warp >> 2) - 1;
+    regs_up<192>();
+    const int g = (warp - SOFTMAX0) / 4;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes 32 * (warp % 4)
     const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
     const int row = g * 128 + (warp & 3) * 32 + lane;
-    int ns = 0, no = 0;
+    uint32_t sp = 0, op = 0, mp = 0;  // parities
     bool ok = true;
-    while (cur.left > 0 && ok) {
+    // the group's four warps, with a bounded wait
+    auto together = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meet[g]);
+      ok = warp_wait(&meet[g], mp, DEV_TIMEOUT_MMA);
+      mp ^= 1;
+      return ok;
+    };
+    while (cur.left > 0) {
       const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
       if (cur.x.r1 - cur.x.r0 > g * 128) {
         const int r = cur.x.r0 + row;
@@ -449,30 +507,31 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
         const int top = in ? cur.s.ctx - cur.s.n + a.group.token(r) : -1;
         const int bot = a.window > 0 ? top - a.window : -1;
         float m = -INFINITY, l = 0.f;
-        // lane c < 16: the page of keys j + 8 c .. + 7 of a block, read a block ahead (0 where there is no such key)
+        // lane c < 16: the page of keys j + 8 c .. + 7 of a block, read a block ahead (0 where there is none)
         auto fetch_page = [&](int j) {
           j += 8 * lane;
           return lane < 16 && j < end ? __ldg(table + (j >> a.b.page_shift)) : 0;
         };
         int pg = fetch_page(first);
-        for (int i = 0; i < units; ++i, ++ns) {
+        for (int i = 0; i < units; ++i) {
           const int j0 = first + i * UK;
           // runs of eight keys without a page
           const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.b.n_pages);
-          if (i + 1 < units) pg = fetch_page(j0 + UK);
-          ok = warp_wait(&s_full[g], ns & 1, DEV_TIMEOUT_MMA);
+          if (i + 1 < units) pg = fetch_page(first + (i + 1) * UK);
+          ok = warp_wait(&s_full[g], sp, DEV_TIMEOUT_MMA);
           if (!ok) break;
+          sp ^= 1;
           tc_fence_after();
-          uint32_t s[4][32];
+          uint32_t s[UK / 32][32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+          for (int q = 0; q < UK / 32; ++q) tmem_ld32(ts + 32 * q, s[q]);
           tmem_ld_wait();
-          // every key of the block seen by every row of the warp?
+          // every key seen by every row of the warp?
           const bool clean = __all_sync(0xffffffffu, j0 + UK - 1 <= top && j0 > bot) && bad == 0;
           if (!clean) {
             const int hi = top - j0, lo = bot - j0;  // keys lo < c <= hi of the block are seen
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < UK / 32; ++q) {
               // one bit a key
               uint32_t seen = low_bits(hi + 1 - 32 * q) & ~low_bits(lo + 1 - 32 * q);
 #pragma unroll
@@ -488,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           for (int e = 0; e < 32; e += 2)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-          const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          const float top_s = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
           const bool grow = top_s > m + GROW || (i == 0 && top_s > m) || (m == -INFINITY && top_s > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? top_s : m;
@@ -511,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
           uint64_t sum[2] = {0, 0};  // pairs of FP32 sums
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < UK / 32; ++q) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -524,26 +583,27 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
             }
             tmem_st16(ts + 16 * q, pk);
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
           {
             float s0, s1;
             unpack2(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[g]);
         }
         if (!ok) break;
         // the tile's (or the range's) output
-        ok = warp_wait(&o_full[g], no & 1, DEV_TIMEOUT_MMA);
-        if (!ok) break;
-        ++no;
-        tc_fence_after();
         const bool whole = units == cur.x.units;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u == 0 ? 1 : 0);
-        const float inv = whole ? (l > 0.f ? __fdiv_rn(1.f, l) : 0.f) : 1.f;
         const int64_t off = in ? row_offset(cur.s, a.group, cur.hk, r, a.ldo, D) : -1;
+        const int64_t lse_at = row_offset(cur.s, a.group, cur.hk, in ? r : 0, a.n_heads, 1);
+        ok = warp_wait(&o_full[g], op, DEV_TIMEOUT_MMA);
+        if (!ok) break;
+        op ^= 1;
+        tc_fence_after();
+        const float inv = whole ? (l > 0.f ? __fdiv_rn(1.f, l) : 0.f) : 1.f;
         float* part = a.part + part_offset<MT, D>(slot, row, 0);
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -572,30 +632,51 @@ __global__ void __launch_bounds__(THREADS, 1) attend_tile_kernel(const AttnArgs 
           }
         }
         if (in) {
-          if (!whole) {
+          if (!whole)
             *reinterpret_cast<float2*>(a.part + 2 * static_cast<int64_t>(gridDim.x) * MT * D + (slot * MT + row) * 2) =
                 make_float2(m, l);
-          } else if (a.lse) {
-            a.lse[row_offset(cur.s, a.group, cur.hk, r, a.n_heads, 1)] =
-                l > 0.f ? m * LN2 + logf(l) : -INFINITY;
-          }
+          else if (a.lse)
+            a.lse[lse_at] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
         }
       }
-      advance(units);
+      if (!together()) break;  // the cursor has been read
+      if (warp == SOFTMAX0 + 4 * g && lane == 0) next_tile<MT, UK, DEAD>(a, cur, units);
+      if (!together()) break;
     }
   }
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == SOFTMAX0) tmem_dealloc(tmem, 512);
+}
+
+// Tensor map of a plane: features, slots of a page, key heads, pages; a box is 64
+// features of up to TILE_BOX slots, 128-byte swizzled.  Not every plane has one
+// (strides of 0): then the copies are cp.async throughout.
+bool plane_map(CUtensorMap* m, const void* base, const AttnArgs& a, int D, int n_pages) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn || a.b.row_stride <= 0 || a.b.page_stride <= 0 || (a.n_kv_heads > 1 && a.b.head_stride <= 0)) return false;
+  const cuuint32_t page = 1u << a.b.page_shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), page, static_cast<cuuint64_t>(a.n_kv_heads),
+                              static_cast<cuuint64_t>(n_pages)};
+  const int64_t head_stride = a.n_kv_heads > 1 ? a.b.head_stride : a.b.row_stride;
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.b.row_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2,
+                                 static_cast<cuuint64_t>(a.b.page_stride) * 2};
+  const cuuint32_t box[4] = {64, page < TILE_BOX ? page : TILE_BOX, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CT, int D>
 cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
   const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attend_tile_kernel<CT, D>), Lay<D>::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attend_tile_kernel<CT, D>, dim3(ctas), dim3(THREADS), Lay<D>::BYTES, s, a);
+  CUtensorMap kmap = {}, vmap = {};
+  const int tma = plane_map(&kmap, a.k, a, D, a.b.n_pages) && plane_map(&vmap, a.v, a, D, a.b.n_pages);
+  return launch_pdl(attend_tile_kernel<CT, D>, dim3(ctas), dim3(THREADS), Lay<D>::BYTES, s, a, kmap, vmap, tma);
 }
 
 }  // namespace
