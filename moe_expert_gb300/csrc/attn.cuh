@@ -172,17 +172,23 @@ struct RangeScratch {  // in shared memory, used before the function returns onl
   int64_t before, units;
   SeqView s;
   int b;
+  int64_t counted[WARP_SEQS];  // units of a sequence and key head, when the CTA's warps counted them
 };
 template <int MT, int UK, int DEAD, int THREADS>
 __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta, Cursor& cur,
-                                           RangeScratch<THREADS>& sh) {
+                                           RangeScratch<THREADS>& sh, bool counted = false) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t total, u0, before, units;  // of the batch; the range's first; before and in its sequence
   if (a.b.n_seqs <= WARP_SEQS) {
     SeqView s{0, 0, 0, false};
     if (lane < a.b.n_seqs) s = seq_view(a.b, lane);
     if (s.bad && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-    const int64_t mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s), sum = warp_scan(mine);
+    int64_t mine = 0;
+    if (!counted)
+      mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s);
+    else if (lane < a.b.n_seqs)
+      mine = a.n_kv_heads * sh.counted[lane];
+    const int64_t sum = warp_scan(mine);
     total = __shfl_sync(0xffffffffu, sum, 31);
     u0 = range_begin(cta, total, n_cta);
     const uint32_t past = __ballot_sync(0xffffffffu, sum > u0);

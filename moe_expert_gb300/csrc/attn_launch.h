@@ -12,8 +12,13 @@ constexpr int STREAM_MT = 16, STREAM_UK = 64, STREAM_DEAD = 2, STREAM_CTAS_PER_S
 
 // Many rows a key head: tiles of 256 rows, units of 128 keys, one CTA an SM.
 constexpr int TILE_MT = 256, TILE_UK = 128, TILE_DEAD = 2;
-// The hint (new tokens of the longest sequence x heads a key head) above which tiles are taken.
-constexpr int TILE_MIN_ROWS = 32;
+// The hint (new tokens of the longest sequence x heads a key head) above which the
+// large tiles are taken: with more rows than one small tile the streaming kernel
+// reads every key once a tile.  Measured, 8 key heads of 128, device time of a call,
+// streaming / large tiles: 16 rows, 32 sequences of up to 5000 keys 44.6 / 62.0 us;
+// 25 rows 70.1 / 63.4; 64 rows 130 / 62; 25 rows, 8 sequences of up to 500 keys
+// 12.9 / 14.7.
+constexpr int TILE_MIN_ROWS = STREAM_MT;
 
 cudaError_t launch_attend_stream(const AttnArgs& a, int type, int D, int ctas, cudaStream_t s);
 cudaError_t launch_attend_tile(const AttnArgs& a, int type, int D, int ctas, cudaStream_t s);

@@ -222,10 +222,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   pdl_wait();
   Cursor& cur = cursors[warp < SOFTMAX0 ? warp : SOFTMAX0 + (warp - SOFTMAX0) / 4];
-  if (a.b.n_seqs > WARP_SEQS || warp == 0) {
+  RangeScratch<THREADS>& scratch = *reinterpret_cast<RangeScratch<THREADS>*>(sm + L::Q);  // not in use yet
+  const bool counted = a.b.n_seqs <= WARP_SEQS;
+  if (counted) {
+    // a warp a sequence
+    for (int b = warp; b < a.b.n_seqs; b += THREADS / 32) {
+      const int64_t u = seq_units_warp<MT, UK, DEAD>(seq_view(a.b, b), a.group, a.window);
+      if (lane == 0) scratch.counted[b] = u;
+    }
+    __syncthreads();
+  }
+  if (!counted || warp == 0) {
     Cursor at;
-    find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at,
-                                      *reinterpret_cast<RangeScratch<THREADS>*>(sm + L::Q));  // not in use yet
+    find_range<MT, UK, DEAD, THREADS>(a, blockIdx.x, gridDim.x, at, scratch, counted);
     if (warp == 0 && lane < SOFTMAX0 + 2) cursors[lane] = at;
   }
   tc_fence_before();
