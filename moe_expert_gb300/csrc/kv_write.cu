@@ -25,6 +25,21 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int tok = blockIdx.x;
+  const int per_head = a.D >> 4, rot_units = a.rot >> 4, half = a.rot >> 1;
+  const int units = (a.n_heads + 2 * a.n_kv_heads) * per_head;
+  float x[8], y[8];
+  // feature offsets of a unit's two groups of eight, and their values
+  auto fetch = [&](int u, int& h, int& j, int& i0, int& i1) {
+    h = u / per_head, j = u - h * per_head;
+    const bool split = j < rot_units && !a.interleaved;
+    i0 = split ? 8 * j : 16 * j;
+    i1 = split ? half + 8 * j : 16 * j + 8;
+    load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i0, x);
+    load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i1, y);
+  };
+  int h, j, i0, i1, u = threadIdx.x;
+  if (u < units) fetch(u, h, j, i0, i1);  // under way while the token's place is looked up
+
   const int b = seq_of_token(a.b, tok);
   int pos = -1, page = -1;
   bool bad = b < 0;
@@ -37,22 +52,10 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a) {
   }
   if (bad && threadIdx.x == 0) flag_status(a.b.status, DEV_BAD_BATCH);
 
-  const int per_head = a.D >> 4, rot_units = a.rot >> 4, half = a.rot >> 1;
-  const int units = (a.n_heads + 2 * a.n_kv_heads) * per_head;
-  for (int u = threadIdx.x; u < units; u += blockDim.x) {
-    const int h = u / per_head, j = u - h * per_head;
+  while (u < units) {
     const bool is_q = h < a.n_heads, is_v = h >= a.n_heads + a.n_kv_heads;
-    if (!is_q && page < 0) continue;
     const bool turn = !is_v && j < rot_units;
-    // feature offsets of the two groups of eight
-    const bool split = j < rot_units && !a.interleaved;
-    const int i0 = split ? 8 * j : 16 * j;
-    const int i1 = split ? half + 8 * j : 16 * j + 8;
-    float x[8], y[8];
-    if (pos >= 0) {
-      load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i0, x);
-      load8<TYPE>(a.qkv, tok * a.ld + static_cast<int64_t>(h) * a.D + i1, y);
-    } else {
+    if (pos < 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
     }
@@ -78,25 +81,26 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const KvWriteArgs a) {
         }
       }
     }
-    void* dst;
-    int64_t off;
     if (is_q) {
-      dst = a.q;
-      off = tok * a.ldq + static_cast<int64_t>(h) * a.D;
-    } else {
-      const int hk = is_v ? h - a.n_heads - a.n_kv_heads : h - a.n_heads;
-      dst = is_v ? a.v : a.k;
-      off = kv_offset(a.b, page, hk, pos);
+      const int64_t off = tok * a.ldq + static_cast<int64_t>(h) * a.D;
+      store8<CT>(a.q, off + i0, x);
+      store8<CT>(a.q, off + i1, y);
+    } else if (page >= 0) {
+      const int64_t off = kv_offset(a.b, page, is_v ? h - a.n_heads - a.n_kv_heads : h - a.n_heads, pos);
+      store8<CT>(is_v ? a.v : a.k, off + i0, x);
+      store8<CT>(is_v ? a.v : a.k, off + i1, y);
     }
-    store8<CT>(dst, off + i0, x);
-    store8<CT>(dst, off + i1, y);
+    u += blockDim.x;
+    if (u < units) fetch(u, h, j, i0, i1);
   }
 }
 
 template <int TYPE>
 static cudaError_t write_launch(const KvWriteArgs& a, int ct, cudaStream_t s) {
   const int units = (a.n_heads + 2 * a.n_kv_heads) * (a.D / 16);
-  const dim3 grid(a.b.n_tokens), block(units < 256 ? (units + 31) / 32 * 32 : 256);
+  // Many tokens: small CTAs, so that more tokens' look-ups and rows are under way.
+  const int most = a.b.n_tokens > 2 * sm_count() ? 128 : 256;
+  const dim3 grid(a.b.n_tokens), block(units < most ? (units + 31) / 32 * 32 : most);
   return ct == MOEX_BF16 ? launch_pdl(kv_write_kernel<TYPE, MOEX_BF16>, grid, block, 0, s, a)
                          : launch_pdl(kv_write_kernel<TYPE, MOEX_F16>, grid, block, 0, s, a);
 }
