@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -116,13 +117,31 @@ at::Tensor fresh(at::IntArrayRef size, const at::Tensor& like, at::ScalarType ty
   return at::empty(size, like.options().dtype(type));
 }
 
-moex_stream stream_of(PyObject* o, const at::Tensor& t) {
-  if (o == Py_None)
-    return reinterpret_cast<moex_stream>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
-  void* p = PyLong_AsVoidPtr(o);
-  if (!p && PyErr_Occurred()) throw PythonError();
-  return static_cast<moex_stream>(p);
-}
+// The stream of a call: the given handle, else torch's current one.  What is
+// allocated while this lives belongs to that stream, so a workspace that is
+// released when the call returns is not handed to another stream's tensor while
+// the kernels still use it.
+class CallStream {
+ public:
+  CallStream(PyObject* o, const at::Tensor& t) {
+    if (!t.is_cuda()) refuse("every tensor has to be a CUDA tensor");
+    if (o == Py_None) {
+      handle_ = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+      return;
+    }
+    void* p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw PythonError();
+    handle_ = static_cast<cudaStream_t>(p);
+    if (handle_ != c10::cuda::getCurrentCUDAStream(t.device().index()).stream())
+      guard_.emplace(handle_ ? c10::cuda::getStreamFromExternal(handle_, t.device().index())
+                             : c10::cuda::getDefaultCUDAStream(t.device().index()));
+  }
+  operator moex_stream() const { return reinterpret_cast<moex_stream>(handle_); }
+
+ private:
+  cudaStream_t handle_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
+};
 
 void check(moex_status st, const char* what) {
   if (st == MOEX_OK) return;
@@ -168,6 +187,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("add_rms_norm", n, 11, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "x");
     const at::Tensor& gamma = tensor(a[1], "gamma");
+    const CallStream stream(a[10], x);
     if (x.dim() != 2) refuse("x: expected [T, H]");
     const int64_t T = x.size(0), H = x.size(1);
     const int64_t ldx = row_stride(x, T, H, "x");
@@ -200,7 +220,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(moex_add_rms_norm(x.data_ptr(), xt, ldx, residual ? residual->data_ptr<float>() : nullptr, ldr,
                             static_cast<float*>(flat(gamma, H, at::kFloat, "gamma")), static_cast<float>(real(a[2])),
                             count(T, "T"), H, sum ? sum->data_ptr<float>() : nullptr, lds, y ? y->data_ptr() : nullptr,
-                            y ? type_code(y->scalar_type()) : MOEX_F32, ldy, qp, dp, stream_of(a[10], x)),
+                            y ? type_code(y->scalar_type()) : MOEX_F32, ldy, qp, dp, stream),
           "moex_add_rms_norm");
     PyObject* r = PyTuple_New(4);
     if (!r) throw PythonError();
@@ -217,6 +237,7 @@ PyObject* dequantize_q8_1(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("dequantize_q8_1", n, 5, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
     const at::Tensor& ds = tensor(a[1], "ds");
+    const CallStream stream(a[4], q);
     if (q.dim() != 2) refuse("q: expected [T, K]");
     const int64_t T = q.size(0), K = q.size(1);
     auto y = maybe(a[2], "y");
@@ -226,7 +247,7 @@ PyObject* dequantize_q8_1(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!y) y = fresh({T, K}, q, dtype.value_or(at::kFloat));
     check(moex_dequantize_q8_1(static_cast<int8_t*>(qp), static_cast<float*>(dp), count(T, "T"), K,
                                flat(*y, T * K, y->scalar_type(), "y"), type_code(y->scalar_type()),
-                               stream_of(a[4], q)),
+                               stream),
           "moex_dequantize_q8_1");
     return wrap(y);
   });
@@ -236,6 +257,7 @@ PyObject* dequantize_q8_1(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("route_experts", n, 12, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "logits");
+    const CallStream stream(a[11], x);
     if (x.dim() != 2) refuse("logits: expected [T, E]");
     const int64_t T = x.size(0), E = x.size(1);
     const int64_t ldl = row_stride(x, T, E, "logits");
@@ -249,7 +271,7 @@ PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              count(E, "E"), k, int32(a[2], "score"), int32(a[4], "groups"), int32(a[5], "top_groups"),
                              int32(a[6], "group_top"), truth(a[7]) ? 1 : 0, static_cast<float>(real(a[8])),
                              static_cast<int32_t*>(flat(*ids, T * k, at::kInt, "ids")),
-                             static_cast<float*>(flat(*w, T * k, at::kFloat, "w")), stream_of(a[11], x)),
+                             static_cast<float*>(flat(*w, T * k, at::kFloat, "w")), stream),
           "moex_route_experts");
     PyObject* r = PyTuple_New(2);
     if (!r) throw PythonError();
@@ -306,6 +328,7 @@ moex_batch batch_of(PyObject* const* a, int64_t tokens, PyObject* max_q) {
 PyObject* rope_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("rope_kv_write", n, 11, [&]() -> PyObject* {
     const at::Tensor& qkv = tensor(a[0], "qkv");
+    const CallStream stream(a[10], qkv);
     if (qkv.dim() != 2) refuse("qkv: expected [T, (n_heads + 2 * kv_heads) * dim]");
     const int64_t T = qkv.size(0);
     const moex_paged_kv kv = paged_kv(a[1], a[2]);
@@ -328,7 +351,7 @@ PyObject* rope_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (q->scalar_type() != ct) refuse("q: expected the cache's type");
     check(moex_rope_kv_write(qkv.data_ptr(), type_code(qkv.scalar_type()), ld, &kv, &b, heads, csp, n_pos,
                              count(rot, "rot_dim"), truth(a[8]) ? 1 : 0, q->data_ptr(),
-                             token_stride(*q, T, heads, D, "q"), stream_of(a[10], qkv)),
+                             token_stride(*q, T, heads, D, "q"), stream),
           "moex_rope_kv_write");
     return wrap(q);
   });
@@ -347,6 +370,7 @@ PyObject* paged_attention_workspace_bytes(PyObject*, PyObject* const* a, Py_ssiz
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_attention", n, 14, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
+    const CallStream stream(a[13], q);
     if (q.dim() != 3) refuse("q: expected [T, n_heads, dim]");
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
     const moex_paged_kv kv = paged_kv(a[1], a[2]);
@@ -370,7 +394,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                type_code(out->scalar_type()), ldo,
                                lse ? static_cast<float*>(flat(*lse, T * H, at::kFloat, "lse")) : nullptr,
                                ws ? flat(*ws, static_cast<int64_t>(bytes), at::kByte, "ws") : nullptr, bytes,
-                               stream_of(a[13], q)),
+                               stream),
           "moex_paged_attention");
     return wrap(out);
   });

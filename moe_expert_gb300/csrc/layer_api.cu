@@ -63,6 +63,7 @@ moex_status moex_dequantize_q8_1(const int8_t* q, const float* ds, int T, int64_
   if (!q || !ds || !y) return MOEX_EINVAL;
   if (!known_type(y_type)) return MOEX_EUNSUPPORTED;
   if (T < 1 || K < QK || K % QK != 0 || K > (1 << 20)) return MOEX_EINVAL;
+  if (T * K / 1024 >= INT32_MAX) return MOEX_EUNSUPPORTED;  // CTAs of 1024 values
   if (!aligned(q, 16) || !aligned(ds, 8) || !aligned(y, 16)) return MOEX_EALIGN;
   return launch_dequantize_q8_1(q, ds, T, K, y, y_type, stream);
 }

@@ -251,3 +251,24 @@ def test_binding_refusals():
         m.paged_attention(q, p.k, p.v, *b, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(m.MoexError):
         m.paged_attention(q, p.k, p.v, *b, scale=-1.0)
+
+
+def test_workspace_belongs_to_the_given_stream():
+    """Calls on a side stream that allocate their workspace and output, while the
+    current stream takes and overwrites every block that comes free."""
+    import torch
+    m = mx()
+    for n, total in (([1] * 3, [4000, 100, 900]), ([200], [1500])):
+        p = Paged(24, n, total, 2, 128, 32)
+        q = _q(p, 8)
+        want = m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q)
+        need = m.paged_attention_workspace_bytes(p.k, p.v, *p.batch(), n_tokens=p.T, n_heads=8, max_q=p.max_q)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(20):
+            outs.append(m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q, stream=st))
+            junk = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+            del junk
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
