@@ -43,13 +43,15 @@ __device__ __forceinline__ float score_of(float x, int sigmoid, float top, float
 // One warp a token.  A group takes 2^lane_shift neighbouring lanes and a lane
 // PER experts in a row (the last ones of a group may be none), so that a
 // group's rank meets in a few neighbouring lanes and the order of lanes is the
-// order of experts: among equal ranks the first lane, then the first of its
-// experts wins.  An arg-max round is a maximum over the lane's keys, redux.sync
-// over the warp and a ballot; the selected experts' scores are computed again
-// from their logits, a lane each, so no scores are carried through the rounds.
+// order of experts.  The selection: a bound that k keys reach, the few keys that
+// reach it compacted to one a lane, and each one's place by counting the keys
+// before it; the selected experts' scores are computed again from their logits.
+// Instructions bound it: 8192 x 256, 8 groups, top-8 takes 9.2 us (1.3 us at the
+// copy rate); k arg-max rounds over all keys took 12.4 us there.
 // FP32 throughout; expf and IEEE division.
 template <int TYPE, int PER>
 __global__ void __launch_bounds__(128) route_experts_kernel(const RouteArgs a) {
+  __shared__ uint2 found[4][32];  // a warp's candidates: key, expert
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -118,37 +120,77 @@ __global__ void __launch_bounds__(128) route_experts_kernel(const RouteArgs a) {
     }
   }
 
-  int my_id = 0;
-#pragma unroll 1
+  // A bound below the k-th largest key: the k-th largest of the lanes' own
+  // maxima (equal ones taken together, which only lowers it).
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+  uint32_t bound = 0;
   for (int r = 0; r < a.k; ++r) {
-    uint32_t best = key[0];
+    bound = __reduce_max_sync(ALL, best);
+    if (best == bound) best = KEY_NONE;
+  }
+  bound = max(bound, KEY_MASKED);
+  // The keys from there on, usually a few more than k, one a lane, in the order of experts.
+  int count = 0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    const uint32_t m = __reduce_max_sync(ALL, best);
-    const int leader = __ffs(__ballot_sync(ALL, best == m)) - 1;
-    int at = 0;
+  for (int i = 0; i < PER; ++i) count += key[i] >= bound;
+  int at = count;
 #pragma unroll
-    for (int i = PER - 1; i > 0; --i)
-      if (key[i] == m) at = i;
-    if (key[0] == m) at = 0;
-    const int e = __shfl_sync(ALL, e0 + at, leader);
-    if (lane == r) my_id = e;
-    if (lane == leader) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(ALL, at, o);
+    if (lane >= o) at += y;
+  }
+  const int total = __shfl_sync(ALL, at, 31);
+  at -= count;
+  int my_id = 0, rank = lane;
+  if (total <= 32) {
+    uint2* mine = found[threadIdx.x >> 5];
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == at) key[i] = KEY_NONE;
+    for (int i = 0; i < PER; ++i)
+      if (key[i] >= bound) mine[at++] = make_uint2(key[i], e0 + i);
+    __syncwarp();
+    const uint2 c = lane < total ? mine[lane] : make_uint2(KEY_NONE, 0);
+    my_id = static_cast<int>(c.y);
+    // its place: the keys above it, and the equal ones before it
+    rank = lane < total ? 0 : 32;
+    for (int j = 0; j < total; ++j) {
+      const uint32_t other = __shfl_sync(ALL, c.x, j);
+      rank += other > c.x || (other == c.x && j < lane);
+    }
+  } else {
+    // many equal keys: one arg-max a round
+#pragma unroll 1
+    for (int r = 0; r < a.k; ++r) {
+      best = key[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+      const uint32_t m = __reduce_max_sync(ALL, best);
+      const int leader = __ffs(__ballot_sync(ALL, best == m)) - 1;
+      int which = 0;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (key[i] == m) which = i;
+      const int e = __shfl_sync(ALL, e0 + which, leader);
+      if (lane == r) my_id = e;
+      if (lane == leader) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i == which) key[i] = KEY_NONE;
+      }
     }
   }
-  float w = lane < a.k ? score_of(RowElem<TYPE>::get(row[my_id]), a.sigmoid, top, sum) : 0.f;
+  const bool chosen = rank < a.k;
+  float w = chosen ? score_of(RowElem<TYPE>::get(row[my_id]), a.sigmoid, top, sum) : 0.f;
   if (a.renorm) {
-    float total = w;  // k <= 16
+    float all = w;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(ALL, total, o);
-    w = total > 0.f ? __fdiv_rn(w, total) : 0.f;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(ALL, all, o);
+    w = all > 0.f ? __fdiv_rn(w, all) : 0.f;
   }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = my_id;
-    a.w[t * a.k + lane] = w * a.scale;
+  if (chosen) {
+    a.ids[t * a.k + rank] = my_id;
+    a.w[t * a.k + rank] = w * a.scale;
   }
 }
 

@@ -80,6 +80,19 @@ def test_ties_go_to_the_lower_index():
     assert ids[1].tolist() == [0, 1, 2, 3]
 
 
+@pytest.mark.parametrize("E,k,groups", [(1024, 16, 1), (256, 8, 8), (512, 3, 4), (100, 16, 2)])
+def test_few_distinct_logits(E, k, groups):
+    """Hundreds of equal ranks around the k-th: the lowest indices of them."""
+    import torch
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randint(0, 3, (64, E), generator=g).float().cuda()
+    for score in ("softmax", "sigmoid"):
+        ids, w = _run(logits, k, score=score, groups=groups, top_groups=max(1, groups // 2))
+        rid, rw, _ = ol.route_experts(f64(logits), k, score=score, groups=groups, top_groups=max(1, groups // 2))
+        assert np.array_equal(ids, rid)
+        assert np.allclose(w, rw, rtol=1.2e-5, atol=0)
+
+
 def test_bias_moves_the_selection_only():
     import torch
     logits = torch.tensor([[2.0, 1.0, 0.0, -1.0]], device="cuda")
