@@ -1,5 +1,7 @@
 // Causal attention of new tokens over a paged cache: choice of the kernel, its
 // workspace, and the joining of tiles that several CTAs worked on.
+#include <algorithm>
+
 #include "attn.cuh"
 #include "attn_launch.h"
 #include "internal.h"
@@ -176,15 +178,35 @@ namespace {
 // CTAs of a launch and its workspace: their range starts, then two partial tiles each.
 struct AttnGrid {
   bool tile;  // the tcgen05 kernel of 256-row tiles
+  bool cut;   // ranges may cut tiles
   int ctas, mt;
   size_t plan_bytes, bytes;
 };
 
-AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads) {
+AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads, int window) {
   AttnGrid g;
   g.tile = static_cast<int64_t>(b->max_q) * (n_heads / kv->n_kv_heads) > TILE_MIN_ROWS;
   g.mt = g.tile ? TILE_MT : STREAM_MT;
   g.ctas = (g.tile ? 1 : STREAM_CTAS_PER_SM) * sm_count();
+  // The most keys that a tile can see, as far as the host knows.
+  int64_t keys = static_cast<int64_t>(b->table_width) * kv->page_size;
+  if (window > 0) keys = std::min(keys, static_cast<int64_t>(window) + b->max_q);
+  // Short tiles are left whole: no second kernel and no workspace (two launches cost the
+  // host about 2 us more than one), against ranges that are less equal.  Measured, device
+  // time cut / whole: streaming, heads of 128, 64 sequences of up to 250 keys 16.3 / 15.2 us,
+  // 300 keys 16.8 / 13.6, 500 keys 18.8 / 19.2, one sequence of 500 keys 9.3 / 12.7; heads of
+  // 64, 64 sequences of up to 500 keys 15.6 / 12.9, one 8.3 / 9.3.  Large tiles, 0.5 a CTA,
+  // 250 keys 18.1 / 13.8, 550 keys 20.7 / 19.1, 1250 keys 23.7 / 29.6; 1.9 a CTA, 600 keys
+  // 36.1 / 33.2, 1300 keys 47.0 / 51.2; 3.5 a CTA, 1600 keys 82.3 / 79.6.
+  if (g.tile) {
+    const int64_t rows = static_cast<int64_t>(b->n_tokens) * (n_heads / kv->n_kv_heads);
+    const int64_t tiles = kv->n_kv_heads * std::max<int64_t>(b->n_seqs, rows / TILE_MT);
+    g.cut = keys > 384 && keys * g.ctas > 512 * tiles;
+  } else {
+    g.cut = keys * kv->head_dim > 288 * 128;
+  }
+  g.plan_bytes = g.bytes = 0;
+  if (!g.cut) return g;
   g.plan_bytes = (g.ctas * sizeof(RangeStart) + 255) / 256 * 256;
   g.bytes = g.plan_bytes + static_cast<size_t>(2 * g.ctas) * g.mt * (kv->head_dim + 2) * 4;
   return g;
@@ -206,7 +228,7 @@ cudaError_t launch_join(const AttnArgs& a, const AttnGrid& g, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attention_ws_bytes(const moex_paged_kv* kv, const moex_batch* batch, int n_heads) {
-  return grid_of(kv, batch, n_heads).bytes;
+  return grid_of(kv, batch, n_heads, 0).bytes;
 }
 
 moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
@@ -214,7 +236,7 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                                    float* lse, void* ws, cudaStream_t s) {
   uint32_t* status = device_status_ptr();
   if (!status) return MOEX_ECUDA;
-  const AttnGrid g = grid_of(kv, batch, n_heads);
+  const AttnGrid g = grid_of(kv, batch, n_heads, window);
   const AttnArgs a{batch_view(kv, batch, status),
                    q,
                    kv->k,
@@ -230,10 +252,12 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                    kv->n_kv_heads,
                    window,
                    out_type == MOEX_F32,
+                   g.cut,
                    head_group(n_heads / kv->n_kv_heads, batch->n_tokens)};
   const cudaError_t e = g.tile ? launch_attend_tile(a, kv->type, kv->head_dim, g.ctas, s)
                                : launch_attend_stream(a, kv->type, kv->head_dim, g.ctas, s);
   if (e != cudaSuccess) return MOEX_ECUDA;
+  if (!g.cut) return MOEX_OK;
   if (kv->type == MOEX_BF16)
     return cuda_status(kv->head_dim == 64 ? launch_join<MOEX_BF16, 64>(a, g, s)
                                           : launch_join<MOEX_BF16, 128>(a, g, s));

@@ -52,6 +52,7 @@ struct AttnArgs {
   int64_t ldq, ldo;
   float scale_log2;   // scale * log2(e): scores are kept in powers of two
   int n_heads, n_kv_heads, window, out_f32;
+  int cut;            // whether ranges may cut tiles; otherwise a tile is its first unit's CTA's, and plan and part are null
   HeadGroup group;
 };
 
@@ -125,6 +126,30 @@ struct Cursor {
   SeqView s;
   Tile x;
 };
+
+// To the first unit of the next tile; `done` units of this one were in the range.
+template <int MT, int UK, int DEAD>
+__device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int done) {
+  cur.left -= done + DEAD;
+  cur.u = 0;
+  if (cur.left <= 0) return;
+  ++cur.t;
+  if (cur.t * MT >= cur.s.n * a.group.n) {
+    cur.t = 0;
+    if (++cur.hk == a.n_kv_heads) {
+      cur.hk = 0;
+      do {
+        cur.s = seq_view(a.b, ++cur.b);
+      } while (cur.s.n == 0);
+    }
+  }
+  cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
+}
+
+// Units of the tile that are this CTA's, from the cursor on.
+__device__ __forceinline__ int units_here(const AttnArgs& a, const Cursor& cur) {
+  return a.cut ? static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u))) : cur.x.units;
+}
 
 // Inclusive sum over the warp's lanes.
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {
@@ -247,7 +272,7 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   }
   cur.left = range_begin(cta + 1, total, n_cta) - u0;
   if (cur.left == 0) {
-    if (lane == 0) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (lane == 0 && a.cut) a.plan[cta] = RangeStart{total, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   int64_t off = u0 - before;
@@ -276,28 +301,13 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   off -= DEAD;
   if (off < 0) cur.left += off;  // the range begins among the tile's dead units
   cur.u = static_cast<int>(max(off, int64_t(0)));
+  if (!a.cut) {
+    if (cur.u > 0) next_tile<MT, UK, DEAD>(a, cur, cur.x.units - cur.u);
+    return;
+  }
   if (lane == 0)  // of every warp that is here: the same values
     a.plan[cta] = RangeStart{total, tile_u, cur.b, cur.hk, cur.t, cur.u, cur.x.units, cur.x.r1 - cur.x.r0,
                              cur.s.first, cur.s.n, cur.s.ctx, 0};
-}
-
-// To the first unit of the next tile; `done` units of this one were in the range.
-template <int MT, int UK, int DEAD>
-__device__ __forceinline__ void next_tile(const AttnArgs& a, Cursor& cur, int done) {
-  cur.left -= done + DEAD;
-  cur.u = 0;
-  if (cur.left <= 0) return;
-  ++cur.t;
-  if (cur.t * MT >= cur.s.n * a.group.n) {
-    cur.t = 0;
-    if (++cur.hk == a.n_kv_heads) {
-      cur.hk = 0;
-      do {
-        cur.s = seq_view(a.b, ++cur.b);
-      } while (cur.s.n == 0);
-    }
-  }
-  cur.x = tile_of<MT, UK>(cur.s, a.group, a.window, cur.t);
 }
 
 // Offset of row r of a tile's sequence and key head in a packed [token][head][D] buffer.

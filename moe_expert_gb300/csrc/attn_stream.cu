@@ -67,8 +67,8 @@ struct Smem {
 // k0 + i * UK .. + 15.
 struct WarpKeys {
   int units, k0, end, steps;
-  __device__ __forceinline__ WarpKeys(const Cursor& c, int warp) {
-    units = static_cast<int>(min(c.left, static_cast<int64_t>(c.x.units - c.u)));
+  __device__ __forceinline__ WarpKeys(const AttnArgs& a, const Cursor& c, int warp) {
+    units = units_here(a, c);
     const int first = c.x.lo + c.u * UK;
     end = min(c.x.hi, first + units * UK);
     k0 = first + warp * STEP;
@@ -111,14 +111,14 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   auto seek = [&](bool fresh) {
     for (;; fresh = false) {
       if (!fresh) {
-        const int units = WarpKeys(ahead, warp).units;
+        const int units = WarpKeys(a, ahead, warp).units;
         __syncwarp();
         if (lane == 0) next_tile<MT, UK, DEAD>(a, ahead, units);
         __syncwarp();
       }
       l_more = ahead.left > 0;
       if (!l_more) return;
-      const WarpKeys w(ahead, warp);
+      const WarpKeys w(a, ahead, warp);
       if (w.steps == 0) continue;
       l_i = 0, l_steps = w.steps, l_k0 = w.k0, l_end = w.end, l_hk = ahead.hk;
       l_table = a.b.table + ahead.b * a.b.table_stride;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
 
   while (cur.left > 0) {
     const Tile x = cur.x;
-    const WarpKeys w(cur, warp);
+    const WarpKeys w(a, cur, warp);
     const int base = cur.s.ctx - cur.s.n;
     int top[2], bot[2];  // keys bot < j <= top are seen by the row
 #pragma unroll

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     bool ok = true;
     for (int tile = 0; cur.left > 0 && ok; ++tile) {
-      const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+      const int units = units_here(a, cur);
       const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, hk = cur.hk;
       const int32_t* table = a.b.table + cur.b * a.b.table_stride;
       // lane l < 16: the page of run l of a block, read a block ahead and looked at when its turn comes
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_f16_ts_elect(tmem + 256 + g * 128, tmem + g * 128 + 8 * ks, vb + ks * (2048 >> 4), IDESC_O, acc || ks != 0);
       };
       while (cur.left > 0 && ok) {
-        const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+        const int units = units_here(a, cur);
         const int groups = cur.x.r1 - cur.x.r0 > 128 ? 2 : 1;
         ok = warp_wait(q_full, qp, DEV_TIMEOUT_MMA) && warp_wait(&kv_full[kr.slot], kr.parity, DEV_TIMEOUT_MMA);
         if (!ok) break;
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       return ok;
     };
     while (cur.left > 0) {
-      const int units = static_cast<int>(min(cur.left, static_cast<int64_t>(cur.x.units - cur.u)));
+      const int units = units_here(a, cur);
       if (cur.x.r1 - cur.x.r0 > g * 128) {
         const int r = cur.x.r0 + row;
         const bool in = r < cur.x.r1;

@@ -232,7 +232,7 @@ def test_other_stream_and_given_workspace():
 def test_binding_refusals():
     import torch
     m = mx()
-    p = Paged(23, [3], [40], 2, 64, 16)
+    p = Paged(23, [3], [40], 2, 64, 16, extra_width=100)   # wide enough to need a workspace
     q = _q(p, 4)
     b = p.batch()
     for bad in (lambda: m.paged_attention(q, p.k, p.v[:, :1], *b), lambda: m.paged_attention(q.half(), p.k, p.v, *b),
