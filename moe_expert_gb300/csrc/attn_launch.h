@@ -11,8 +11,8 @@ struct AttnArgs;
 // prompts 62.6 / 59.7 / 61.4 / 62.0 / 62.0 us, 64 single tokens 153.7 / 152.3 / 153.5 /
 // 154.7 / 155.6 us.
 
-// Few rows a key head: tiles of 16 rows, units of 64 keys, two CTAs an SM.
-constexpr int STREAM_MT = 16, STREAM_UK = 64, STREAM_DEAD = 2, STREAM_CTAS_PER_SM = 2;
+// Few rows a key head: tiles of 16 rows, two CTAs an SM.
+constexpr int STREAM_MT = 16, STREAM_DEAD = 2, STREAM_CTAS_PER_SM = 2;
 
 // Many rows a key head: tiles of 256 rows, units of 128 keys, one CTA an SM.
 constexpr int TILE_MT = 256, TILE_UK = 128, TILE_DEAD = 2;

@@ -2,11 +2,11 @@
 // is streamed once, so DRAM bounds it.
 //
 // A CTA of four warps works on one tile of 16 rows; each warp runs alone
-// over every fourth step of 16 keys, with its own copies in flight (cp.async,
-// no CTA barrier in the loop), its own running maximum and sum, and the
-// products on mma.sync m16n8k16: with 16 rows a step of 16 keys is 8 KB of cache
-// and 32 such instructions, far below the tensor rate, and tcgen05's 128-row
-// tiles would be mostly empty.  The copies run on from one tile into the next;
+// over every fourth step of 16 keys (32 with heads of 64: 8 KB of cache either
+// way), with its own copies in flight (cp.async, no CTA barrier in the loop), its
+// own running maximum and sum, and the products on mma.sync m16n8k16: with 16
+// rows a step is 32 such instructions, far below the tensor rate, and tcgen05's
+// 128-row tiles would be mostly empty.  The copies run on from one tile into the next;
 // the four warps' results meet in shared memory at the end of a tile.
 #include "attn.cuh"
 #include "attn_launch.h"
@@ -15,9 +15,8 @@
 namespace moex {
 namespace {
 
-constexpr int MT = STREAM_MT, UK = STREAM_UK, DEAD = STREAM_DEAD;
-constexpr int WARPS = 4, STEP = 16, STAGES = 2;
-static_assert(UK == WARPS * STEP, "a unit is one step of every warp");
+constexpr int MT = STREAM_MT, DEAD = STREAM_DEAD;
+constexpr int WARPS = 4, STAGES = 2;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -57,6 +56,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // [WARPS][MT][D + 4] with their maxima and sums at the end of a tile.
 template <int D>
 struct Smem {
+  static constexpr int STEP = D == 64 ? 32 : 16;  // keys of a step
+  static constexpr int UK = WARPS * STEP;         // keys of a unit: a step of every warp
   static constexpr int PLANE = STEP * D * 2;   // bytes of a step's keys
   static constexpr int RING = WARPS * STAGES * 2 * PLANE;
   static constexpr int PITCH = D + 4;          // floats of an output row
@@ -65,6 +66,7 @@ struct Smem {
 
 // The keys of a tile that a CTA's range holds, as one warp sees them: steps
 // k0 + i * UK .. + 15.
+template <int STEP, int UK>
 struct WarpKeys {
   int units, k0, end, steps;
   __device__ __forceinline__ WarpKeys(const AttnArgs& a, const Cursor& c, int warp) {
@@ -81,6 +83,8 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   extern __shared__ __align__(128) uint8_t sm[];
   using S = Smem<D>;
   using E = RowElem<CT>;
+  constexpr int STEP = S::STEP, UK = S::UK, RUNS = STEP / 8;  // runs of eight keys, each inside one page
+  using Keys = WarpKeys<STEP, UK>;
   constexpr int CH = D / 8;     // 16-byte chunks of a row
   constexpr int KS = D / 16;    // k-steps of the first product
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -100,25 +104,25 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   __syncwarp();
   int l_i = 0, l_steps = 0, l_k0 = 0, l_end = 0, l_hk = 0;  // the tile that copies are issued for
   bool l_more = true;
-  int pg0 = -1, pg1 = -1;  // lane l: pages of step 32 * (l_i / 32) + l, its first and second eight keys
+  int pg[RUNS];  // lane l: pages of the runs of step 32 * (l_i / 32) + l
   const int32_t* l_table = nullptr;
   auto fetch_pages = [&]() {
     const int j = l_k0 + (l_i + lane) * UK;
-    pg0 = j < l_end ? __ldg(l_table + (j >> a.b.page_shift)) : -1;
-    pg1 = j + 8 < l_end ? __ldg(l_table + ((j + 8) >> a.b.page_shift)) : pg0;
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) pg[r] = j + 8 * r < l_end ? __ldg(l_table + ((j + 8 * r) >> a.b.page_shift)) : 0;
   };
   // the next tile in which this warp has a step; its pages are asked for at once
   auto seek = [&](bool fresh) {
     for (;; fresh = false) {
       if (!fresh) {
-        const int units = WarpKeys(a, ahead, warp).units;
+        const int units = Keys(a, ahead, warp).units;
         __syncwarp();
         if (lane == 0) next_tile<MT, UK, DEAD>(a, ahead, units);
         __syncwarp();
       }
       l_more = ahead.left > 0;
       if (!l_more) return;
-      const WarpKeys w(a, ahead, warp);
+      const Keys w(a, ahead, warp);
       if (w.steps == 0) continue;
       l_i = 0, l_steps = w.steps, l_k0 = w.k0, l_end = w.end, l_hk = ahead.hk;
       l_table = a.b.table + ahead.b * a.b.table_stride;
@@ -126,27 +130,37 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
       return;
     }
   };
-  uint32_t ok_ring = 0;  // two bits a stage: the step's halves have a page
+  uint32_t ok_ring = 0;  // RUNS bits a stage: the step's runs have a page
   auto load = [&](int stage) {
     if (l_more) {
       const int j = l_k0 + l_i * UK;
-      int a0 = __shfl_sync(0xffffffffu, pg0, l_i & 31), a1 = __shfl_sync(0xffffffffu, pg1, l_i & 31);
-      if (static_cast<uint32_t>(a0) >= static_cast<uint32_t>(a.b.n_pages) ||
-          static_cast<uint32_t>(a1) >= static_cast<uint32_t>(a.b.n_pages)) {
-        if (lane == 0) flag_status(a.b.status, DEV_BAD_BATCH);
-        if (a0 >= a.b.n_pages) a0 = -1;
-        if (a1 >= a.b.n_pages) a1 = -1;
+      int page[RUNS];
+      uint32_t ok = (1u << RUNS) - 1;
+      bool good = true;
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r) {
+        page[r] = __shfl_sync(0xffffffffu, pg[r], l_i & 31);
+        good = good && static_cast<uint32_t>(page[r]) < static_cast<uint32_t>(a.b.n_pages);
       }
-      ok_ring = (ok_ring & ~(3u << (2 * stage))) | ((a0 >= 0 ? 1u : 0u) | (a1 >= 0 ? 2u : 0u)) << (2 * stage);
+      if (!good) {
+        if (lane == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r)
+          if (static_cast<uint32_t>(page[r]) >= static_cast<uint32_t>(a.b.n_pages)) {
+            page[r] = -1;
+            ok &= ~(1u << r);
+          }
+      }
+      ok_ring = (ok_ring & ~(((1u << RUNS) - 1) << (RUNS * stage))) | ok << (RUNS * stage);
       const uint32_t dst = ring + stage * 2 * S::PLANE;
       constexpr int RPI = 32 / CH;  // rows an instruction covers
       const int c = lane % CH;
 #pragma unroll
       for (int n = 0; n < STEP / RPI; ++n) {
-        const int r = n * RPI + lane / CH;
-        const int page = r < 8 ? a0 : a1;
-        const bool in = j + r < l_end && page >= 0;
-        const int64_t off = in ? kv_offset(a.b, page, l_hk, j + r) + 8 * c : 0;
+        // the run of an instruction's rows is known when this is compiled: RPI divides 8
+        const int r = n * RPI + lane / CH, run = n * RPI / 8;
+        const bool in = j + r < l_end && page[run] >= 0;
+        const int64_t off = in ? kv_offset(a.b, page[run], l_hk, j + r) + 8 * c : 0;
         const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
         cp_async16(at, static_cast<const uint16_t*>(a.k) + off, in ? 16u : 0u);
         cp_async16(at + S::PLANE, static_cast<const uint16_t*>(a.v) + off, in ? 16u : 0u);
@@ -182,7 +196,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
 
   while (cur.left > 0) {
     const Tile x = cur.x;
-    const WarpKeys w(a, cur, warp);
+    const Keys w(a, cur, warp);
     const int base = cur.s.ctx - cur.s.n;
     int top[2], bot[2];  // keys bot < j <= top are seen by the row
 #pragma unroll
@@ -196,27 +210,30 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     for (int i = 0; i < w.steps; ++i) {
-      const uint32_t ok = (ok_ring >> (2 * stage)) & 3u;
+      const uint32_t ok = (ok_ring >> (RUNS * stage)) & ((1u << RUNS) - 1);
       __syncwarp();  // the stage refilled next has been read by every lane
       load(stage ^ 1);
       cp_wait<1>();
       __syncwarp();  // every lane's copies have landed
       const uint32_t kb = ring + stage * 2 * S::PLANE, vb = kb + S::PLANE;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const int r = (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
+      float s[RUNS][4];
+#pragma unroll
+      for (int nt = 0; nt < RUNS; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < RUNS / 2; ++kk) {
+        const int r = 16 * kk + (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t f[4];
           ldsm4(f, kb + r * (D * 2) + (((2 * ks + c) ^ (r & 7)) << 4));
-          mma16816<CT>(s[0], qf[ks], f[0], f[1]);
-          mma16816<CT>(s[1], qf[ks], f[2], f[3]);
+          mma16816<CT>(s[2 * kk], qf[ks], f[0], f[1]);
+          mma16816<CT>(s[2 * kk + 1], qf[ks], f[2], f[3]);
         }
       }
       const int j = w.k0 + i * UK;
       float mx[2] = {m[0], m[1]};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < RUNS; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int half = e >> 1, key = j + 8 * nt + p2 + (e & 1);
@@ -235,7 +252,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
         m[half] = mx[half];
         l[half] *= corr[half];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < RUNS; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float pv = fast_exp2(s[nt][2 * half + e] - ref);
@@ -243,11 +260,19 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
             l[half] += pv;
           }
       }
-      // probabilities rounded to the cache type: the A operand of the second product
-      const uint32_t pf[4] = {E::pack(s[0][0], s[0][1]), E::pack(s[0][2], s[0][3]), E::pack(s[1][0], s[1][1]),
-                              E::pack(s[1][2], s[1][3])};
-      {
-        const int r = ((lane >> 3) & 1) * 8 + (lane & 7), c = lane >> 4;
+      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+        for (int i2 = 0; i2 < D / 8; ++i2) {
+          o[i2][0] *= corr[0], o[i2][1] *= corr[0], o[i2][2] *= corr[1], o[i2][3] *= corr[1];
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < RUNS / 2; ++kk) {
+        // probabilities rounded to the cache type: the A operand of the second product
+        const uint32_t pf[4] = {E::pack(s[2 * kk][0], s[2 * kk][1]), E::pack(s[2 * kk][2], s[2 * kk][3]),
+                                E::pack(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                                E::pack(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+        const int r = 16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), c = lane >> 4;
 #pragma unroll
         for (int nt = 0; nt < D / 16; ++nt) {
           uint32_t f[4];
@@ -255,7 +280,6 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float(&od)[4] = o[2 * nt + h];
-            od[0] *= corr[0], od[1] *= corr[0], od[2] *= corr[1], od[3] *= corr[1];
             mma16816<CT>(od, pf, f[2 * h], f[2 * h + 1]);
           }
         }

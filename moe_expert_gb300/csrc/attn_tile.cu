@@ -10,15 +10,21 @@
 // Warps: 0 issues the MMAs; 1-3 copy keys, values and queries; 4-7 and 8-11 are
 // the softmax of the two groups, one row a thread, so maxima and sums need no
 // exchange (192 registers: a row's 128 scores stay in them).  A block of keys
-// comes by TMA, a box for each page and 64 features (the issuing lanes take no
-// time from the softmax, which cp.async address arithmetic did: 398 -> 345 us for
-// 2048 tokens over 14336 keys with 32 heads); a block that the sequence does not
-// fill, or that has a page out of range, comes by cp.async with zeros in place of
-// what is not there, since a value beside a probability of 0 must be finite.
+// comes by cp.async, or by TMA where pages are long enough.
+// A block that the sequence does not fill, or that has a page out of range, comes
+// by cp.async with zeros in place of what is not there, since a value beside a
+// probability of 0 must be finite.
 // The MMA order is PV0(j), QK0(j+1), PV1(j), QK1(j+1): while one group's
 // products run the other's softmax does.  A row's reference for the exponentials
 // follows its maximum only when that grows by more than 2^8, so O is rescaled
 // rarely; sums and O are exact for any reference.
+// Measured, 2048 tokens over 14336 keys, 32 heads of 128, 8 key heads, pages of
+// 64: 325-342 us with the joining kernel on four boxes, 1505-1587 TFLOP/s (floor
+// 268 us); the tensor pipe works 70% of the kernel's time.  The chain softmax - PV
+// - QK of a group, about 2800 cycles a block against 2048 of tensor work for both
+// groups, sets the pace.  Slower: two threads a row (375 us), P handed over in
+// halves (363 us), the same softmax in 176 registers beside four copying warps
+// (408 us).
 #include "attn.cuh"
 #include "attn_launch.h"
 #include "internal.h"
@@ -28,7 +34,7 @@ namespace moex {
 namespace {
 
 constexpr int MT = TILE_MT, UK = TILE_UK, DEAD = TILE_DEAD;
-constexpr int TILE_BOX = 64;  // slots of a TMA box at most
+constexpr int MIN_BOX = 32, MAX_BOX = 64;  // slots of a TMA box
 constexpr int THREADS = 384, LOADERS = 3, SOFTMAX0 = 4;  // warps 1-3 copy, 4-11 softmax
 constexpr float GROW = 8.f;  // log2 of the growth of a maximum that rescales O
 
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const uint32_t dst = smb + L::RING + ring.slot * L::STAGE;
           if (whole && tma) {
-            // every key of the block is there: boxes of one page, 64 features wide, a lane a box
+            // every key of the block is there: boxes of a page's slots and 64 features, a lane a box
             if (untold) {
               cp_wait<0>();
               announce(0);
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lw == 0) {
               if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], L::STAGE);
               __syncwarp();
-              const int box = min(1 << a.b.page_shift, TILE_BOX), part = lane % (D / 64), key = lane / (D / 64) * box;
+              const int box = min(1 << a.b.page_shift, MAX_BOX), part = lane % (D / 64), key = lane / (D / 64) * box;
               const int page = __shfl_sync(0xffffffffu, pages, (key >> 3) & 15);
               if (key < UK)
                 tma_load_4d(dst + part * L::HALF + key * 128, kv ? &vmap : &kmap, 64 * part,
@@ -660,19 +666,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == SOFTMAX0) tmem_dealloc(tmem, 512);
 }
 
-// Tensor map of a plane: features, slots of a page, key heads, pages; a box is 64
-// features of up to TILE_BOX slots, 128-byte swizzled.  Not every plane has one
-// (strides of 0): then the copies are cp.async throughout.
+// Tensor map of a plane: features, slots of a page, key heads, pages.  Pages of
+// fewer than MIN_BOX slots have none, since shorter boxes are bound by the box rate
+// (the chunk measured above took 350 us with cp.async at any page size, by TMA
+// 325 us with pages of 64, 353 us with 32, 450 us with 16; packed prompts with pages
+// of 32 61.4 and 59.8 us), nor have strides of 0; then the copies are cp.async
+// throughout.
 bool plane_map(CUtensorMap* m, const void* base, const AttnArgs& a, int D, int n_pages) {
   const EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn || a.b.row_stride <= 0 || a.b.page_stride <= 0 || (a.n_kv_heads > 1 && a.b.head_stride <= 0)) return false;
+  if (!fn || (1 << a.b.page_shift) < MIN_BOX || a.b.row_stride <= 0 || a.b.page_stride <= 0 || (a.n_kv_heads > 1 && a.b.head_stride <= 0)) return false;
   const cuuint32_t page = 1u << a.b.page_shift;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), page, static_cast<cuuint64_t>(a.n_kv_heads),
                               static_cast<cuuint64_t>(n_pages)};
   const int64_t head_stride = a.n_kv_heads > 1 ? a.b.head_stride : a.b.row_stride;
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.b.row_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2,
                                  static_cast<cuuint64_t>(a.b.page_stride) * 2};
-  const cuuint32_t box[4] = {64, page < TILE_BOX ? page : TILE_BOX, 1, 1};
+  const cuuint32_t box[4] = {64, page < MAX_BOX ? page : MAX_BOX, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
