@@ -185,7 +185,8 @@ struct AttnGrid {
 
 AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads, int window) {
   AttnGrid g;
-  g.tile = static_cast<int64_t>(b->max_q) * (n_heads / kv->n_kv_heads) > TILE_MIN_ROWS;
+  g.tile = static_cast<int64_t>(b->max_q) * (n_heads / kv->n_kv_heads) >
+           (kv->head_dim == 64 ? TILE_MIN_ROWS_64 : TILE_MIN_ROWS);
   g.mt = g.tile ? TILE_MT : STREAM_MT;
   g.ctas = (g.tile ? 1 : STREAM_CTAS_PER_SM) * sm_count();
   // The most keys that a tile can see, as far as the host knows.
