@@ -500,7 +500,10 @@ size_t moex_paged_attention_workspace_bytes(const moex_paged_kv* kv, const moex_
  *   lse = log sum_j exp(scale * q.k_j).
  * Scores, their maximum and sum, and the accumulated output are FP32;
  * probabilities are rounded to the cache type for the second product.  A token
- * that sees no key gives zeros and lse = -inf.
+ * that sees no key gives zeros and lse = -inf.  What lies in the cache past a
+ * sequence's length, or in pages of others, has no influence whatever its bits;
+ * values that a sequence's new tokens see should be finite (an infinity or NaN
+ * that one of them sees may reach the others, which multiply it by 0).
  *   q    : device [n_tokens][n_heads][head_dim] of the cache type, token t at q + t*ldq.
  *   out  : device [n_tokens][n_heads][head_dim] of out_type (the cache type or
  *          F32), token t at out + t*ldo.
@@ -509,7 +512,8 @@ size_t moex_paged_attention_workspace_bytes(const moex_paged_kv* kv, const moex_
  *          NULL when that is 0.
  * head_dim 64 or 128; n_heads a multiple of n_kv_heads, at most 128 a key
  * head; scale > 0; ldq and ldo multiples of 8.  Results do not depend on the
- * order in which blocks run.
+ * order in which blocks run.  Two launches, or one when the page table holds few
+ * keys a sequence (no workspace then).
  */
 moex_status moex_paged_attention(const void* q, int64_t ldq, const moex_paged_kv* kv, const moex_batch* batch,
                                  int n_heads, float scale, int window, void* out, int out_type, int64_t ldo, float* lse,
