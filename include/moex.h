@@ -500,7 +500,8 @@ size_t moex_paged_attention_workspace_bytes(const moex_paged_kv* kv, const moex_
  *   lse = log sum_j exp(scale * q.k_j).
  * Scores, their maximum and sum, and the accumulated output are FP32;
  * probabilities are rounded to the cache type for the second product.  A token
- * that sees no key gives zeros and lse = -inf.  What lies in the cache past a
+ * that sees no key gives zeros and lse = -inf; a NaN in a query gives NaN in
+ * both, for that token and head alone.  What lies in the cache past a
  * sequence's length, or in pages of others, has no influence whatever its bits;
  * values that a sequence's new tokens see should be finite (an infinity or NaN
  * that one of them sees may reach the others, which multiply it by 0).

@@ -101,8 +101,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * D / 4) attend_join_kernel(const At
   v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
   store_out4<CT>(a, row_offset(s, a.group, x.hk, x.t * MT + r, a.ldo, D) + 4 * c, v);
   if (a.lse && c == 0)
-    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] =
-        l > 0.f ? top[r] * LN2 + logf(l) : -INFINITY;
+    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = row_lse(top[r], l);
 }
 
 // The same for tiles of many rows, which few ranges cut: a thread has 16 columns
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(2 * D) attend_join_rows_kernel(const AttnArgs 
       store8<CT>(a.out, off + 8 * h, o);
   }
   if (a.lse && c0 == 0)
-    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
+    a.lse[row_offset(s, a.group, x.hk, x.t * MT + r, a.n_heads, 1)] = row_lse(m, l);
 }
 
 namespace {

@@ -64,6 +64,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Log of a row's sum l of exponentials relative to 2^m: -inf for a row without
+// keys; a NaN among the scores is in l, though the maximum passes over it.
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : m * LN2 + logf(l); }
+
 // One tile of a sequence's rows and the keys that its rows see.
 struct Tile {
   int r0, r1;  // rows

@@ -334,8 +334,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
         store_out4<CT>(a, row_offset(seq, a.group, hk, x.r0 + r, a.ldo, D) + c, acc);
         if (a.lse && c == 0)
-          a.lse[row_offset(seq, a.group, hk, x.r0 + r, a.n_heads, 1)] =
-              ll > 0.f ? mm * LN2 + logf(ll) : -INFINITY;
+          a.lse[row_offset(seq, a.group, hk, x.r0 + r, a.n_heads, 1)] = row_lse(mm, ll);
       } else {
         *reinterpret_cast<float4*>(a.part + part_offset<MT, D>(slot, r, c)) = acc;
         if (c == 0) {

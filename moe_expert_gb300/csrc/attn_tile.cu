@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             *reinterpret_cast<float2*>(a.part + 2 * static_cast<int64_t>(gridDim.x) * MT * D + (slot * MT + row) * 2) =
                 make_float2(m, l);
           else if (a.lse)
-            a.lse[lse_at] = l > 0.f ? m * LN2 + logf(l) : -INFINITY;
+            a.lse[lse_at] = row_lse(m, l);
         }
       }
       if (!together()) break;  // the cursor has been read

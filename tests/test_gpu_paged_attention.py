@@ -212,6 +212,25 @@ def test_bad_batches_are_flagged_and_left_out():
         assert torch.equal(m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q), good) and status() == 0
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,total", [([1, 2, 1], [90, 40, 17]),          # few rows, tiles left whole
+                                     ([1, 2, 1], [3000, 40, 900]),       # few rows, tiles cut
+                                     ([100, 30], [140, 30]),             # many rows, tiles left whole
+                                     ([100, 30], [2900, 700])])          # many rows, tiles cut
+def test_nan_in_a_query_stays_in_its_row(n, total, dim):
+    import torch
+    m = mx()
+    p = Paged(24, n, total, 2, dim, 16)
+    q = _q(p, 8)
+    lse, clean_lse = (torch.empty(p.T, 8, device="cuda") for _ in range(2))
+    clean = m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q, lse=clean_lse)
+    q[1, 3, 5] = float("nan")
+    out = m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q, lse=lse)
+    assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3])
+    out[1, 3], lse[1, 3] = clean[1, 3], clean_lse[1, 3]
+    assert torch.equal(out, clean) and torch.equal(lse, clean_lse) and status() == 0
+
+
 def test_other_stream_and_given_workspace():
     import torch
     m = mx()
