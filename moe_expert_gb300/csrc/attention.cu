@@ -236,6 +236,7 @@ moex_status launch_paged_attention(const void* q, int64_t ldq, const moex_paged_
                                    float* lse, void* ws, cudaStream_t s) {
   uint32_t* status = device_status_ptr();
   if (!status) return MOEX_ECUDA;
+  if (window >= 1 << 30) window = 0;  // sees every position, and position - window may leave 32 bits
   const AttnGrid g = grid_of(kv, batch, n_heads, window);
   const AttnArgs a{batch_view(kv, batch, status),
                    q,

@@ -231,6 +231,17 @@ def test_nan_in_a_query_stays_in_its_row(n, total, dim):
     assert torch.equal(out, clean) and torch.equal(lse, clean_lse) and status() == 0
 
 
+@pytest.mark.parametrize("n,total,Hq", [([10, 1], [5, 300], 4), ([300, 30], [295, 700], 2)])
+def test_largest_window_is_no_window(n, total, Hq):
+    import torch
+    m = mx()
+    p = Paged(25, n, total, 2, 64, 16)     # the first tokens have negative positions
+    q = _q(p, Hq)
+    want = m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q)
+    for window in ((1 << 30) - 1, 1 << 30, (1 << 31) - 1):
+        assert torch.equal(m.paged_attention(q, p.k, p.v, *p.batch(), max_q=p.max_q, window=window), want)
+
+
 def test_other_stream_and_given_workspace():
     import torch
     m = mx()
