@@ -5,6 +5,7 @@
 
 #include <cmath>
 
+#include "attn_launch.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -118,8 +119,8 @@ moex_status moex_paged_attention(const void* q, int64_t ldq, const moex_paged_kv
   if (!(scale > 0.f) || !std::isfinite(scale) || window < 0) return MOEX_EINVAL;
   if (ldq < static_cast<int64_t>(n_heads) * kv->head_dim || ldo < static_cast<int64_t>(n_heads) * kv->head_dim)
     return MOEX_EINVAL;
-  // row indices (token within its sequence, head of the group) are 32-bit
-  if (static_cast<int64_t>(batch->n_tokens) * n_heads > INT32_MAX) return MOEX_EUNSUPPORTED;
+  // row indices (token within its sequence, head of the group) are 32-bit, those of the last tile's end too
+  if (static_cast<int64_t>(batch->n_tokens) * n_heads > INT32_MAX - 2 * TILE_MT) return MOEX_EUNSUPPORTED;
   const size_t need = paged_attention_ws_bytes(kv, batch, n_heads);
   if (ws_bytes < need || (need > 0 && !ws)) return MOEX_ENOSPACE;
   if (ldq % 8 != 0 || ldo % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 16))

@@ -132,6 +132,18 @@ def test_attention_refusals():
         assert f(n=need - 1) == ENOSPACE and f(ws=NULL) == ENOSPACE and f(ws=odd) == EALIGN
 
 
+def test_attention_refuses_rows_past_32_bits():
+    import moe_expert_gb300 as mx
+    L = ensure_lib()
+    buf, base, p, odd = _p()
+    kv = _kv(mx, base, n_kv_heads=1)
+    # 128 heads: 2^31 - 128 rows fit 32 bits, the end of the last tile does not
+    for n in (1 << 24, (1 << 24) - 1, (1 << 24) - 4):
+        b = _batch(mx, base, n_tokens=n, max_q=1)
+        assert L.moex_paged_attention(p, 1 << 13, ctypes.byref(kv), ctypes.byref(b), 128, 0.125, 0, p, 1, 1 << 13, NULL,
+                                      p, 1 << 40, NULL) == EUNSUPPORTED, n
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     torch = pytest.importorskip("torch")
     import moe_expert_gb300 as mx
