@@ -231,13 +231,16 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
     int64_t mine = 0, first = 0;
     SeqView s{0, 0, 0, false};
     total = 0;
-    // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit
+    // pass 0 finds W (and keeps the one block of a small batch); pass 1 the place of the range's first unit.
+    // `it` counts the blocks of both passes: neighbouring blocks use different halves of warp_sum, also where
+    // one pass ends and the other begins, so a half is written again only after a barrier behind its readers.
+    int it = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       const int64_t want = pass ? range_begin(cta, total, n_cta) : 0;
       int64_t run = 0;
 #pragma unroll 1
-      for (int base = 0, it = 0; base < a.b.n_seqs; base += THREADS, ++it) {
+      for (int base = 0; base < a.b.n_seqs; base += THREADS, ++it) {
         const int b = base + threadIdx.x;
         if (pass == 0 || a.b.n_seqs > THREADS) {
           s = SeqView{0, 0, 0, false};
