@@ -502,8 +502,10 @@ size_t moex_paged_attention_workspace_bytes(const moex_paged_kv* kv, const moex_
  * probabilities are rounded to the cache type for the second product.  A token
  * that sees no key gives zeros and lse = -inf; a NaN in a query gives NaN in
  * both, for that token and head alone.  What lies in the cache past a
- * sequence's length, or in pages of others, has no influence whatever its bits;
- * values that a sequence's new tokens see should be finite (an infinity or NaN
+ * sequence's length, in front of the window of all its new tokens, or in pages
+ * of others, has no influence whatever its bits, and pages wholly in front of
+ * that window are not asked for: their entries in page_table may be anything.
+ * Values that a sequence's new tokens see should be finite (an infinity or NaN
  * that one of them sees may reach the others, which multiply it by 0).
  *   q    : device [n_tokens][n_heads][head_dim] of the cache type, token t at q + t*ldq.
  *   out  : device [n_tokens][n_heads][head_dim] of out_type (the cache type or

@@ -72,6 +72,7 @@ __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -
 struct Tile {
   int r0, r1;  // rows
   int lo, hi;  // keys [lo, hi)
+  int from;    // the first key that a row sees: those in front of it may be anything, and their pages gone
   int units;   // at least one, so that rows without keys are written too
 };
 
@@ -82,11 +83,11 @@ __device__ __forceinline__ Tile tile_of(const SeqView& s, const HeadGroup& group
   x.r1 = min(s.n * group.n, x.r0 + MT);
   const int base = s.ctx - s.n;
   x.hi = max(base + group.token(x.r1 - 1) + 1, 0);
+  x.from = window > 0 ? min(max(base + group.token(x.r0) - window + 1, 0), x.hi) : 0;
   // whole runs of eight keys for the copies; in the kernel of large tiles whole blocks, so that a block
   // begins where a box of the cache does
   constexpr int ALIGN = MT >= 128 ? UK : 16;
-  x.lo = window > 0 ? max(base + group.token(x.r0) - window + 1, 0) & ~(ALIGN - 1) : 0;
-  x.lo = min(x.lo, x.hi & ~(ALIGN - 1));
+  x.lo = x.from & ~(ALIGN - 1);
   x.units = max((x.hi - x.lo + UK - 1) / UK, 1);
   return x;
 }

@@ -78,8 +78,10 @@ struct WarpKeys {
   }
 };
 
+// The bound on registers is that of the two CTAs an SM gets: with what the compiler
+// takes by itself (128 for heads of 64) a few spill.
 template <int CT, int D>
-__global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, STREAM_CTAS_PER_SM) attend_stream_kernel(const AttnArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   using S = Smem<D>;
   using E = RowElem<CT>;
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, p2 = 2 * (lane & 3);
   pdl_wait();
-  pdl_launch_dependents();  // the joining kernel's CTAs fit beside these, and wait
+  pdl_launch_dependents();  // the joining kernel's CTAs take the place of these as they end, and wait
   Cursor cur;
   __shared__ RangeScratch<WARPS * 32> scratch;
   find_range<MT, UK, DEAD, WARPS * 32>(a, blockIdx.x, gridDim.x, cur, scratch);
@@ -109,7 +111,10 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
   auto fetch_pages = [&]() {
     const int j = l_k0 + (l_i + lane) * UK;
 #pragma unroll
-    for (int r = 0; r < RUNS; ++r) pg[r] = j + 8 * r < l_end ? __ldg(l_table + ((j + 8 * r) >> a.b.page_shift)) : 0;
+    for (int r = 0; r < RUNS; ++r) {
+      const int k = j + 8 * r;
+      pg[r] = k + 7 >= ahead.x.from && k < l_end ? __ldg(l_table + (k >> a.b.page_shift)) : 0;
+    }
   };
   // the next tile in which this warp has a step; its pages are asked for at once
   auto seek = [&](bool fresh) {
@@ -153,13 +158,15 @@ __global__ void __launch_bounds__(WARPS * 32) attend_stream_kernel(const AttnArg
       }
       ok_ring = (ok_ring & ~(((1u << RUNS) - 1) << (RUNS * stage))) | ok << (RUNS * stage);
       const uint32_t dst = ring + stage * 2 * S::PLANE;
+      const int r0 = ahead.x.from - j, r1 = l_end - j;  // the step's rows that are there
       constexpr int RPI = 32 / CH;  // rows an instruction covers
       const int c = lane % CH;
 #pragma unroll
       for (int n = 0; n < STEP / RPI; ++n) {
         // the run of an instruction's rows is known when this is compiled: RPI divides 8
         const int r = n * RPI + lane / CH, run = n * RPI / 8;
-        const bool in = j + r < l_end && page[run] >= 0;
+        // zeros in place of keys outside: a value beside a probability of 0 must be finite
+        const bool in = r >= r0 && r < r1 && page[run] >= 0;
         const int64_t off = in ? kv_offset(a.b, page[run], l_hk, j + r) + 8 * c : 0;
         const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
         cp_async16(at, static_cast<const uint16_t*>(a.k) + off, in ? 16u : 0u);

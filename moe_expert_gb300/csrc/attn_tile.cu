@@ -11,9 +11,9 @@
 // the softmax of the two groups, one row a thread, so maxima and sums need no
 // exchange (192 registers: a row's 128 scores stay in them).  A block of keys
 // comes by cp.async, or by TMA where pages are long enough.
-// A block that the sequence does not fill, or that has a page out of range, comes
-// by cp.async with zeros in place of what is not there, since a value beside a
-// probability of 0 must be finite.
+// A block that the sequence or its window does not fill, or that has a page out
+// of range, comes by cp.async with zeros in place of what no row sees or is not
+// there, since a value beside a probability of 0 must be finite.
 // The MMA order is PV0(j), QK0(j+1), PV1(j), QK1(j+1): while one group's
 // products run the other's softmax does.  A row's reference for the exponentials
 // follows its maximum only when that grows by more than 2^8, so O is rescaled
@@ -298,10 +298,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int units = units_here(a, cur);
       const int first = cur.x.lo + cur.u * UK, hi = cur.x.hi, hk = cur.hk;
       const int32_t* table = a.b.table + cur.b * a.b.table_stride;
-      // lane l < 16: the page of run l of a block, read a block ahead and looked at when its turn comes
+      // lane l < 16: the page of run l of a block, read a block ahead and looked at when its turn comes;
+      // a run wholly in front of the window or behind the keys has none
+      auto has_page = [&](int j) { return lane < 16 && j + 7 >= cur.x.from && j < hi; };
       auto fetch_page = [&](int j) {
         j += 8 * lane;
-        return lane < 16 && j < hi ? __ldg(table + (j >> a.b.page_shift)) : -1;
+        return has_page(j) ? __ldg(table + (j >> a.b.page_shift)) : -1;
       };
       int pg = fetch_page(first);
       for (int i = 0; i < units; ++i) {
@@ -310,10 +312,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         int64_t mine = -1;
         if (pg >= 0 && pg < a.b.n_pages)
           mine = kv_offset(a.b, pg, hk, j);
-        else if (lane < 16 && j < hi)
+        else if (has_page(j))
           flag_status(a.b.status, DEV_BAD_BATCH);
         const int pages = pg;  // of this block's runs
-        const bool whole = __all_sync(0xffffffffu, lane >= 16 || mine >= 0) && j0 + UK <= hi;
+        const bool whole = __all_sync(0xffffffffu, lane >= 16 || (mine >= 0 && j >= cur.x.from)) && j0 + UK <= hi;
         if (i + 1 < units) pg = fetch_page(j0 + UK);
         int64_t off[RUNS];
 #pragma unroll
@@ -365,9 +367,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int run = lw; run < 16; run += LOADERS) {
               const int64_t at = __shfl_sync(0xffffffffu, mine, run);
+              const int k0 = cur.x.from - j0 - 8 * run - r0, k1 = hi - j0 - 8 * run - r0;
 #pragma unroll
               for (int k = 0; k < PER_RUN; ++k) {
-                const bool in = at >= 0 && j0 + 8 * run + k * RPI + r0 < hi;
+                const bool in = at >= 0 && k * RPI >= k0 && k * RPI < k1;
                 cp_async16(dst + dst0[k] + run * 1024, in ? src + at + k * rows : src - mine_at, in ? 16u : 0u);
               }
             }
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int pg = fetch_page(first);
         for (int i = 0; i < units; ++i) {
           const int j0 = first + i * UK;
-          // runs of eight keys without a page
+          // runs of eight keys without a page (also such as no row sees: masked twice)
           const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.b.n_pages);
           if (i + 1 < units) pg = fetch_page(first + (i + 1) * UK);
           ok = warp_wait(&s_full[g], sp, DEV_TIMEOUT_MMA);
