@@ -73,17 +73,23 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   if (ss <= FLT_MAX || isnan(ss)) {
     rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.H)) + a.eps));
   } else {
-    // The squares left FP32's range: once more on the row scaled by 2^-64 (eps is
-    // nothing beside them), which brings every finite row back into it.
-    constexpr float DOWN = 5.421010862427522e-20f;
+    // The squares left FP32's range: once more on the row scaled by 2^-96.  Values are
+    // then below 2^32, so 32768 squares fit; and one of the row's is above 2^56 here
+    // (2^128 over 32768 squares), so the sum is above 2^-80.  The product with 1 / sqrt
+    // is taken before the scaling, which is exact, so small values lose no bits.
+    constexpr float DOWN = 1.2621774483536189e-29f;
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      v[i].x *= DOWN, v[i].y *= DOWN, v[i].z *= DOWN, v[i].w *= DOWN;
-      ss += v[i].x * v[i].x + v[i].y * v[i].y + (v[i].z * v[i].z + v[i].w * v[i].w);
+      const float4 d = make_float4(v[i].x * DOWN, v[i].y * DOWN, v[i].z * DOWN, v[i].w * DOWN);
+      ss += d.x * d.x + d.y * d.y + (d.z * d.z + d.w * d.w);
     }
     ss = cta_sum(ss, part[1]);
-    rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.H))));
+    rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.H)) + a.eps * DOWN * DOWN));
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      v[i] = make_float4(v[i].x * rstd * DOWN, v[i].y * rstd * DOWN, v[i].z * rstd * DOWN, v[i].w * rstd * DOWN);
+    rstd = 1.f;
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
