@@ -1,6 +1,7 @@
 // A batch of sequences over a paged cache, as kernels see it.
 #pragma once
 
+#include "batch_clip.h"
 #include "common.cuh"
 
 namespace moex {
@@ -35,22 +36,9 @@ inline BatchView batch_view(const moex_paged_kv* kv, const moex_batch* b, uint32
   return v;
 }
 
-// One sequence's new tokens and length, cut to what the batch can hold: its
-// tokens are first .. first + n - 1 and token i has position ctx - n + i.
-struct SeqView {
-  int first, n, ctx;
-  bool bad;  // something had to be cut
-};
-
+// The tokens and length of sequence b (table_width pages are at most 2^30 positions by the host's check).
 __device__ __forceinline__ SeqView seq_view(const BatchView& v, int b) {
-  SeqView s;
-  const int lo = v.cu_q[b], hi = v.cu_q[b + 1], ctx = v.ctx_len[b];
-  const int most = v.table_width << v.page_shift;  // below 2^30 by the host's check
-  s.first = min(max(lo, 0), v.n_tokens);
-  s.n = max(min(hi, v.n_tokens) - s.first, 0);
-  s.ctx = min(max(ctx, 0), most);
-  s.bad = s.first != lo || hi < lo || hi > v.n_tokens || s.ctx != ctx;
-  return s;
+  return clip_seq(v.cu_q[b], v.cu_q[b + 1], v.ctx_len[b], v.n_tokens, v.table_width << v.page_shift);
 }
 
 // The sequence that token `tok` belongs to, or -1.
