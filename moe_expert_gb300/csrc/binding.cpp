@@ -76,10 +76,6 @@ std::optional<at::ScalarType> maybe_dtype(PyObject* o) {
   return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
-void on_gpu(const at::Tensor& t, const char* what) {
-  if (!t.is_cuda()) refuse(std::string(what) + ": every tensor has to be a CUDA tensor");
-}
-
 int32_t count(int64_t n, const char* what) {
   if (n > INT32_MAX) refuse(std::string(what) + ": too large");
   return static_cast<int32_t>(n);
@@ -88,7 +84,6 @@ int32_t count(int64_t n, const char* what) {
 // Row stride of a matrix of rows x width with contiguous rows (the width for a
 // single row, whose stride says nothing).
 int64_t row_stride(const at::Tensor& t, int64_t rows, int64_t width, const char* what) {
-  on_gpu(t, what);
   if (t.dim() != 2 || t.size(0) != rows || t.size(1) != width || (width > 1 && t.stride(1) != 1))
     refuse(std::string(what) + ": expected [" + std::to_string(rows) + ", " + std::to_string(width) +
            "], rows contiguous");
@@ -96,7 +91,6 @@ int64_t row_stride(const at::Tensor& t, int64_t rows, int64_t width, const char*
 }
 
 void* flat(const at::Tensor& t, int64_t numel, at::ScalarType type, const char* what) {
-  on_gpu(t, what);
   if (t.numel() != numel || t.scalar_type() != type || !t.is_contiguous())
     refuse(std::string(what) + ": expected " + std::to_string(numel) + " contiguous elements of " +
            c10::toString(type));
@@ -105,7 +99,6 @@ void* flat(const at::Tensor& t, int64_t numel, at::ScalarType type, const char* 
 
 // Token stride of [tokens][heads][dim] with contiguous tokens.
 int64_t token_stride(const at::Tensor& t, int64_t tokens, int64_t heads, int64_t dim, const char* what) {
-  on_gpu(t, what);
   if (t.dim() != 3 || t.size(0) != tokens || t.size(1) != heads || t.size(2) != dim || t.stride(2) != 1 ||
       (heads > 1 && t.stride(1) != dim))
     refuse(std::string(what) + ": expected [" + std::to_string(tokens) + ", " + std::to_string(heads) + ", " +
@@ -117,28 +110,52 @@ at::Tensor fresh(at::IntArrayRef size, const at::Tensor& like, at::ScalarType ty
   return at::empty(size, like.options().dtype(type));
 }
 
-// The stream of a call: the given handle, else torch's current one.  What is
-// allocated while this lives belongs to that stream, so a workspace that is
-// released when the call returns is not handed to another stream's tensor while
-// the kernels still use it.
+// The device of a call, current while this lives: the launch, the allocations and
+// the status word are that device's, whichever was current.  Every tensor among
+// the call's arguments has to be on it.
+class CallDevice {
+ public:
+  CallDevice(PyObject* const* a, Py_ssize_t n, const at::Tensor& first) {
+    const at::Device device = first.device();
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      // what is plainly no tensor first: for those the check itself is a slow one
+      if (a[i] == Py_None || PyLong_Check(a[i]) || PyFloat_Check(a[i]) || THPDtype_Check(a[i]) ||
+          !THPVariable_Check(a[i]))
+        continue;
+      const at::Tensor& t = THPVariable_Unpack(a[i]);
+      if (!t.is_cuda()) refuse("every tensor has to be a CUDA tensor");
+      if (t.device() != device)
+        refuse("every tensor has to be on one device: " + device.str() + " and " + t.device().str());
+    }
+    if (c10::cuda::current_device() != device.index()) guard_.set_device(device);
+  }
+
+ private:
+  c10::cuda::OptionalCUDAGuard guard_;
+};
+
+// The stream of a call on that device: the handle in the last argument, else
+// torch's current one.  What is allocated while this lives belongs to that stream,
+// so a workspace that is released when the call returns is not handed to another
+// stream's tensor while the kernels still use it.
 class CallStream {
  public:
-  CallStream(PyObject* o, const at::Tensor& t) {
-    if (!t.is_cuda()) refuse("every tensor has to be a CUDA tensor");
-    if (o == Py_None) {
-      handle_ = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
-      return;
-    }
+  CallStream(PyObject* const* a, Py_ssize_t n, const at::Tensor& first) : device_(a, n, first) {
+    PyObject* const o = a[n - 1];
+    const auto index = first.device().index();
+    handle_ = c10::cuda::getCurrentCUDAStream(index).stream();
+    if (o == Py_None) return;
     void* p = PyLong_AsVoidPtr(o);
     if (!p && PyErr_Occurred()) throw PythonError();
-    handle_ = static_cast<cudaStream_t>(p);
-    if (handle_ != c10::cuda::getCurrentCUDAStream(t.device().index()).stream())
-      guard_.emplace(handle_ ? c10::cuda::getStreamFromExternal(handle_, t.device().index())
-                             : c10::cuda::getDefaultCUDAStream(t.device().index()));
+    const cudaStream_t given = static_cast<cudaStream_t>(p);
+    if (given == handle_) return;
+    handle_ = given;
+    guard_.emplace(handle_ ? c10::cuda::getStreamFromExternal(handle_, index) : c10::cuda::getDefaultCUDAStream(index));
   }
   operator moex_stream() const { return reinterpret_cast<moex_stream>(handle_); }
 
  private:
+  CallDevice device_;
   cudaStream_t handle_;
   std::optional<c10::cuda::CUDAStreamGuard> guard_;
 };
@@ -187,7 +204,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("add_rms_norm", n, 11, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "x");
     const at::Tensor& gamma = tensor(a[1], "gamma");
-    const CallStream stream(a[10], x);
+    const CallStream stream(a, n, x);
     if (x.dim() != 2) refuse("x: expected [T, H]");
     const int64_t T = x.size(0), H = x.size(1);
     const int64_t ldx = row_stride(x, T, H, "x");
@@ -237,7 +254,7 @@ PyObject* dequantize_q8_1(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("dequantize_q8_1", n, 5, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
     const at::Tensor& ds = tensor(a[1], "ds");
-    const CallStream stream(a[4], q);
+    const CallStream stream(a, n, q);
     if (q.dim() != 2) refuse("q: expected [T, K]");
     const int64_t T = q.size(0), K = q.size(1);
     auto y = maybe(a[2], "y");
@@ -257,7 +274,7 @@ PyObject* dequantize_q8_1(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("route_experts", n, 12, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "logits");
-    const CallStream stream(a[11], x);
+    const CallStream stream(a, n, x);
     if (x.dim() != 2) refuse("logits: expected [T, E]");
     const int64_t T = x.size(0), E = x.size(1);
     const int64_t ldl = row_stride(x, T, E, "logits");
@@ -284,8 +301,6 @@ PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
 moex_paged_kv paged_kv(PyObject* ko, PyObject* vo) {
   const at::Tensor& k = tensor(ko, "k_cache");
   const at::Tensor& v = tensor(vo, "v_cache");
-  on_gpu(k, "k_cache");
-  on_gpu(v, "v_cache");
   if (k.dim() != 4 || v.scalar_type() != k.scalar_type() || v.sizes() != k.sizes() || v.strides() != k.strides() ||
       k.stride(3) != 1)
     refuse("k_cache and v_cache: the same type, shape [pages, heads, page, dim] and strides, dim contiguous");
@@ -308,7 +323,6 @@ moex_batch batch_of(PyObject* const* a, int64_t tokens, PyObject* max_q) {
   const at::Tensor& cu = tensor(a[0], "cu_q");
   const at::Tensor& ctx = tensor(a[1], "ctx_len");
   const at::Tensor& table = tensor(a[2], "page_table");
-  on_gpu(table, "page_table");
   if (table.dim() != 2 || table.scalar_type() != at::kInt || (table.size(1) > 1 && table.stride(1) != 1))
     refuse("page_table: expected int32 [B, width], rows contiguous");
   moex_batch b;
@@ -328,7 +342,7 @@ moex_batch batch_of(PyObject* const* a, int64_t tokens, PyObject* max_q) {
 PyObject* rope_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("rope_kv_write", n, 11, [&]() -> PyObject* {
     const at::Tensor& qkv = tensor(a[0], "qkv");
-    const CallStream stream(a[10], qkv);
+    const CallStream stream(a, n, qkv);
     if (qkv.dim() != 2) refuse("qkv: expected [T, (n_heads + 2 * kv_heads) * dim]");
     const int64_t T = qkv.size(0);
     const moex_paged_kv kv = paged_kv(a[1], a[2]);
@@ -360,6 +374,7 @@ PyObject* rope_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (k_cache, v_cache, cu_q, ctx_len, page_table, n_tokens, n_heads, max_q) -> bytes
 PyObject* paged_attention_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_attention_workspace_bytes", n, 8, [&]() -> PyObject* {
+    const CallDevice device(a, n, tensor(a[0], "k_cache"));
     const moex_paged_kv kv = paged_kv(a[0], a[1]);
     const moex_batch b = batch_of(a + 2, int32(a[5], "n_tokens"), a[7]);
     return PyLong_FromSize_t(moex_paged_attention_workspace_bytes(&kv, &b, int32(a[6], "n_heads")));
@@ -370,7 +385,7 @@ PyObject* paged_attention_workspace_bytes(PyObject*, PyObject* const* a, Py_ssiz
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_attention", n, 14, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
-    const CallStream stream(a[13], q);
+    const CallStream stream(a, n, q);
     if (q.dim() != 3) refuse("q: expected [T, n_heads, dim]");
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
     const moex_paged_kv kv = paged_kv(a[1], a[2]);
