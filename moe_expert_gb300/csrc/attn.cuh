@@ -64,6 +64,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Powers of two that a row's reference for the exponentials lies below its
+// maximum, when the maximum may pass it by another 2^grow.  FP16 has most of its
+// range above 1 and holds no more than 2^15: taken up, a probability of 2^-29 of
+// the largest (with grow 0) still has FP16's 11 bits, where it would be dropped from
+// the output, though not from the sum, below 2^-25.  BF16 has FP32's range.
+template <int CT>
+constexpr float prob_up(float grow) {
+  return CT == MOEX_F16 ? 15.f - grow : 0.f;
+}
+
 // Log of a row's sum l of exponentials relative to 2^m: -inf for a row without
 // keys; a NaN among the scores is in l, though the maximum passes over it.
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : m * LN2 + logf(l); }

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(WARPS * 32, STREAM_CTAS_PER_SM) attend_stream_
       bot[half] = a.window > 0 ? top[half] - a.window : -1;
     }
 
+    // m: the row's reference, its maximum but for prob_up
     float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(WARPS * 32, STREAM_CTAS_PER_SM) attend_stream_
         }
       }
       const int j = w.k0 + i * UK;
-      float mx[2] = {m[0], m[1]};
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int nt = 0; nt < RUNS; ++nt)
 #pragma unroll
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(WARPS * 32, STREAM_CTAS_PER_SM) attend_stream_
       for (int half = 0; half < 2; ++half) {
         mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
         mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+        mx[half] = fmaxf(m[half], mx[half] - prob_up<CT>(0.f));
         // a row that has seen no key keeps 0 as its reference, so that -inf - -inf does not arise
         const float ref = mx[half] == -INFINITY ? 0.f : mx[half];
         corr[half] = fast_exp2(m[half] - ref);

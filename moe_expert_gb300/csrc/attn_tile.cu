@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; e += 2)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-          const float top_s = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+          const float top_s = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2 - prob_up<CT>(GROW);
           const bool grow = top_s > m + GROW || (i == 0 && top_s > m) || (m == -INFINITY && top_s > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? top_s : m;
