@@ -451,8 +451,8 @@ typedef struct moex_paged_kv {
  * max_q is the largest number of new tokens of a sequence (it picks the
  * kernel; a wrong value costs time, not results).  What the arrays say is
  * checked on the device: a page id outside [0, n_pages), a length beyond
- * table_width pages or tokens beyond n_tokens are left out and flagged
- * (MOEX_EDEVICE).
+ * table_width pages, tokens beyond n_tokens or tokens of no sequence are left
+ * out and flagged (MOEX_EDEVICE).
  */
 typedef struct moex_batch {
   int32_t n_seqs;

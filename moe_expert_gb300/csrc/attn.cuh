@@ -221,8 +221,10 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
   int64_t total, u0, before, units;  // of the batch; the range's first; before and in its sequence
   if (a.b.n_seqs <= WARP_SEQS) {
     SeqView s{0, 0, 0, false};
-    if (lane < a.b.n_seqs) s = seq_view(a.b, lane);
-    if (s.bad && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+    if (lane < a.b.n_seqs) {
+      s = seq_view(a.b, lane);
+      if (cta == 0 && (s.bad || uncovered(a.b, lane))) flag_status(a.b.status, DEV_BAD_BATCH);
+    }
     int64_t mine = 0;
     if (!counted)
       mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s);
@@ -255,8 +257,10 @@ __device__ __forceinline__ void find_range(const AttnArgs& a, int cta, int n_cta
         const int b = base + threadIdx.x;
         if (pass == 0 || a.b.n_seqs > THREADS) {
           s = SeqView{0, 0, 0, false};
-          if (b < a.b.n_seqs) s = seq_view(a.b, b);
-          if (s.bad && pass == 0 && cta == 0) flag_status(a.b.status, DEV_BAD_BATCH);
+          if (b < a.b.n_seqs) {
+            s = seq_view(a.b, b);
+            if (cta == 0 && pass == 0 && (s.bad || uncovered(a.b, b))) flag_status(a.b.status, DEV_BAD_BATCH);
+          }
           mine = a.n_kv_heads * lane_units<MT, UK, DEAD>(a, s);
           const int64_t x = warp_scan(mine);
           if (lane == 31) sh.warp_sum[it & 1][warp] = x;

@@ -41,6 +41,12 @@ __device__ __forceinline__ SeqView seq_view(const BatchView& v, int b) {
   return clip_seq(v.cu_q[b], v.cu_q[b + 1], v.ctx_len[b], v.n_tokens, v.table_width << v.page_shift);
 }
 
+// Whether tokens in front of the first sequence or behind the last, as sequence
+// b's offsets show it, belong to none.
+__device__ __forceinline__ bool uncovered(const BatchView& v, int b) {
+  return (b == 0 && v.cu_q[b] != 0) || (b + 1 == v.n_seqs && v.cu_q[b + 1] != v.n_tokens);
+}
+
 // The sequence that token `tok` belongs to, or -1.
 __device__ __forceinline__ int seq_of_token(const BatchView& v, int tok) {
   int lo = 0, hi = v.n_seqs;  // the first b with cu_q[b + 1] > tok
