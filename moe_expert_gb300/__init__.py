@@ -514,8 +514,9 @@ def paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q: Optio
                     stream=None):
     """Causal attention of the sequences' new tokens q [T, n_heads, dim] over
     their paged cache (see rope_kv_write for the batch; the cache holds the new
-    tokens already).  max_q: the largest number of new tokens of a sequence
-    (None: T); it picks the kernel.  scale: 1/sqrt(dim) unless given; window >
+    tokens already).  max_q: the largest number of new tokens of a sequence; it
+    picks the kernel (None: T - B + 1, the most that B sequences of one token or
+    more can have; T when T < B).  scale: 1/sqrt(dim) unless given; window >
     0: only the last `window` keys.  Returns out [T, n_heads, dim] of q's type,
     or float32 with out_dtype; lse (float32 [T, n_heads]) is filled when given."""
     return (_native_module or _load_native()).paged_attention(q, k_cache, v_cache, cu_q, ctx_len, page_table, max_q,

@@ -329,7 +329,11 @@ moex_batch batch_of(PyObject* const* a, int64_t tokens, PyObject* max_q) {
   const int64_t n = table.size(0);
   b.n_seqs = count(n, "sequences");
   b.n_tokens = count(tokens, "tokens");
-  b.max_q = max_q == nullptr || max_q == Py_None ? b.n_tokens : int32(max_q, "max_q");
+  // without a hint, the most that sequences of one token or more can have: single tokens are seen as such
+  if (max_q == nullptr || max_q == Py_None)
+    b.max_q = b.n_tokens < b.n_seqs ? b.n_tokens : b.n_tokens - b.n_seqs + 1;
+  else
+    b.max_q = int32(max_q, "max_q");
   b.table_width = count(table.size(1), "page table width");
   b.table_stride = n > 1 ? table.stride(0) : table.size(1);
   b.cu_q = static_cast<int32_t*>(flat(cu, n + 1, at::kInt, "cu_q"));
