@@ -363,7 +363,8 @@ moex_status moex_moe_decode_noalloc(const moex_qweight* gate_up, const moex_qwei
  *   s = x + residual (FP32; s = x without a residual)
  *   y = s * gamma / sqrt(mean(s^2) + eps)
  * and any of three outputs of it: s itself, y as rows, y as q8_1 blocks (the
- * arithmetic of moex_quantize_q8_1 on the FP32 y, one launch instead of two).
+ * arithmetic of moex_quantize_q8_1 on the FP32 y, one launch instead of two;
+ * where amax / 127 is subnormal, values beyond 127 of it are held at +-127).
  *   x        : device [T][H] of x_type (F32, BF16, F16), row t at x + t*ldx.
  *   residual : device FP32, row t at residual + t*ldr, or NULL.
  *   gamma    : device FP32 [H].   eps > 0.

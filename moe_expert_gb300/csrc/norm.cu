@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
       uint32_t packed = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int qi = d > 0.f ? static_cast<int>(roundf(__fdiv_rn(f[j], d))) : 0;
+        // (a subnormal d may be a third too small, a value then up to 190 of it)
+        const int qi = d > 0.f ? min(max(static_cast<int>(roundf(__fdiv_rn(f[j], d))), -127), 127) : 0;
         sum += qi;
         packed |= (static_cast<uint32_t>(qi) & 0xFFu) << (8 * j);
       }

@@ -1,4 +1,5 @@
-"""The norm of rows whose squares leave FP32's range, up to the largest values.
+"""The norm of rows whose squares leave FP32's range, up to the largest values, and
+q8_1 blocks of the smallest.
 The bounds are those of the ordinary rows (test_gpu_norm.py): the scaling by a
 power of two is exact.  Beside a value of 2^128 others give results below 2^-126,
 where even the nearest FP32 number is off by up to 2^-150 (BF16: 2^-134): there
@@ -69,3 +70,20 @@ def test_eps_beside_large_values():
     x = torch.zeros(1, 32768, device="cuda")
     x[0, :2] = 1.5e19
     _check(x, torch.ones(32768, device="cuda"), eps=1e34)
+
+
+def test_smallest_values_do_not_wrap():
+    """Below FP32's smallest normal number amax / 127 rounds to few units, and a
+    value may be more than 127 of them: it is then held as +-127."""
+    import torch
+    m = mx()
+    unit = 2.0 ** -149
+    sign = torch.ones(1, 32, device="cuda")
+    sign[0, 1::2] = -1
+    for units in (64, 100, 127, 150, 190, 250, 1000, 100000):
+        gamma = torch.full((32,), units * unit, device="cuda")
+        _, y, q, ds = m.add_rms_norm(sign, gamma, 1e-30, y_dtype=torch.float32, quantize=True)
+        assert (y.sign() == sign).all()
+        d = ds[0, 0, 0].item()
+        want = 0 if d == 0 else min(127, int(y.abs().max().item() / d + 0.5))
+        assert (q.abs() == want).all() and (q * sign >= 0).all(), units
