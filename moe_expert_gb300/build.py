@@ -3,7 +3,8 @@ and the Python extension module over it with the host compiler.
 
 Every .cu under csrc/ is compiled for sm_103a only, in parallel, then linked
 into one shared library.  csrc/binding.cpp is compiled beside them against
-Python's and torch's headers into _native.so, which links to libmoex.so.
+Python's and torch's headers into _native.so, which links to libmoex.so; where
+there is no torch, the library alone is built, and a message says so.
 Objects go to moe_expert_gb300/_build/.  Run as
 ``python -m moe_expert_gb300.build`` or call ``build()``.
 """
@@ -62,10 +63,10 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
-def _torch_dir() -> str:
+def _torch_dir():
     spec = importlib.util.find_spec("torch")  # without the cost of importing it
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the Python binding is built against it")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
@@ -95,7 +96,7 @@ def _link_binding() -> None:
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Compiles every source, links libmoex.so and the extension module; returns the library's path."""
+    """Compiles every source, links libmoex.so and (with torch) the extension module; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     digest = _headers_digest()
@@ -108,7 +109,13 @@ def build(verbose: bool = False, extra=()) -> str:
             todo.append(s)
     jobs = [lambda s=s: _compile(s, list(extra)) for s in todo]
     bobj = os.path.join(BUILD, "binding.cpp.o")
-    if old != digest or not os.path.exists(bobj) or os.path.getmtime(bobj) < os.path.getmtime(BINDING):
+    binding = _torch_dir() is not None
+    if not binding:
+        sys.stderr.write("torch not found: libmoex.so is built without the Python binding _native.so\n")
+        for p in (bobj, NATIVE):  # of another build of the library
+            if os.path.exists(p):
+                os.remove(p)
+    elif old != digest or not os.path.exists(bobj) or os.path.getmtime(bobj) < os.path.getmtime(BINDING):
         jobs.append(_compile_binding)
     if jobs:
         with cf.ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
@@ -120,7 +127,8 @@ def build(verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding()
+    if binding:
+        _link_binding()
     with open(stamp, "w") as f:
         f.write(digest)
     if verbose:
