@@ -13,6 +13,13 @@
 // tile costs about as much as some units (its queries, its output), so every
 // tile counts DEAD units more than it has, in front of its own: the share of a
 // CTA with many short tiles holds fewer keys.
+//
+// Scores, maxima, sums and outputs are FP32.  Probabilities are rounded to the
+// cache type for the product with the values: the 16-bit tensor instructions take
+// no wider operand beside 16-bit values, and carrying the rest in a second product
+// would double that half of the work.  Each is off by at most 2^-8 (BF16) or 2^-11
+// (FP16) of itself, as a value of the cache is, whatever the output's type; the sum
+// takes them unrounded.
 #pragma once
 
 #include "batch.cuh"
@@ -56,8 +63,19 @@ struct AttnArgs {
   HeadGroup group;
 };
 
+// A copy of 16 bytes to shared memory; bytes 0: zeros, and src is not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 constexpr float LN2 = 0.6931471805599453f;
 
+// 2^x within 2^-22 of it, far below the probabilities' rounding; 0 below 2^-126.
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

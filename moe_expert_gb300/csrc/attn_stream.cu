@@ -18,14 +18,6 @@ namespace {
 constexpr int MT = STREAM_MT, DEAD = STREAM_DEAD;
 constexpr int WARPS = 4, STAGES = 2;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -65,7 +57,7 @@ struct Smem {
 };
 
 // The keys of a tile that a CTA's range holds, as one warp sees them: steps
-// k0 + i * UK .. + 15.
+// k0 + i * UK .. + STEP - 1.
 template <int STEP, int UK>
 struct WarpKeys {
   int units, k0, end, steps;
@@ -277,7 +269,7 @@ __global__ void __launch_bounds__(WARPS * 32, STREAM_CTAS_PER_SM) attend_stream_
       }
 #pragma unroll
       for (int kk = 0; kk < RUNS / 2; ++kk) {
-        // probabilities rounded to the cache type: the A operand of the second product
+        // probabilities rounded to the cache type (attn.cuh): the A operand of the second product
         const uint32_t pf[4] = {E::pack(s[2 * kk][0], s[2 * kk][1]), E::pack(s[2 * kk][2], s[2 * kk][3]),
                                 E::pack(s[2 * kk + 1][0], s[2 * kk + 1][1]),
                                 E::pack(s[2 * kk + 1][2], s[2 * kk + 1][3])};

@@ -2,7 +2,7 @@
 // tcgen05 TMEM allocation, MMA issue / commit, TMEM loads and stores, the
 // shared-memory matrix descriptor, the instruction descriptor, and 2-D TMA
 // tile loads, the CTA-pair (cta_group::2) forms and the cluster barrier
-// helpers they need.  Used by the prefill grouped GEMM.
+// helpers they need.  Used by the prefill grouped GEMM and paged attention.
 #pragma once
 
 #include <cuda.h>
