@@ -193,9 +193,10 @@ AttnGrid grid_of(const moex_paged_kv* kv, const moex_batch* b, int n_heads, int 
   if (window > 0) keys = std::min(keys, static_cast<int64_t>(window) + b->max_q);
   // Short tiles are left whole: no second kernel and no workspace (two launches cost the
   // host about 2 us more than one), against ranges that are less equal.  Measured, device
-  // time cut / whole: streaming, heads of 128, 64 sequences of up to 250 keys 16.3 / 15.2 us,
-  // 300 keys 16.8 / 13.6, 500 keys 18.8 / 19.2, one sequence of 500 keys 9.3 / 12.7; heads of
-  // 64, 64 sequences of up to 500 keys 15.6 / 12.9, one 8.3 / 9.3.  Large tiles, 0.5 a CTA,
+  // time cut / whole: streaming, heads of 128, 64 sequences of up to 250 keys 14.8 / 11.7 us,
+  // 300 keys 15.2 / 13.0, 500 keys 16.9 / 14.8, one sequence of 250 keys 8.7 / 7.2, 500 keys
+  // 9.3 / 10.2; heads of 64, 64 sequences of up to 500 keys 14.1 / 11.8, 600 keys 14.8 / 13.3,
+  // one of 500 8.3 / 7.4.  Large tiles, 0.5 a CTA,
   // 250 keys 18.1 / 13.8, 550 keys 20.7 / 19.1, 1250 keys 23.7 / 29.6; 1.9 a CTA, 600 keys
   // 36.1 / 33.2, 1300 keys 47.0 / 51.2; 3.5 a CTA, 1600 keys 82.3 / 79.6.
   if (g.tile) {

@@ -19,7 +19,7 @@
 // follows its maximum only when that grows by more than 2^8, so O is rescaled
 // rarely; sums and O are exact for any reference.
 // Measured, 2048 tokens over 14336 keys, 32 heads of 128, 8 key heads, pages of
-// 64: 325-344 us with the joining kernel on six boxes, 1497-1587 TFLOP/s (floor
+// 64: 323-344 us with the joining kernel on ten boxes, 1497-1596 TFLOP/s (floor
 // 268 us); the tensor pipe works 70% of the kernel's time.  The chain softmax - PV
 // - QK of a group, about 2800 cycles a block against 2048 of tensor work for both
 // groups, sets the pace.  Slower: two threads a row (375 us), P handed over in
