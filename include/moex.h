@@ -525,7 +525,8 @@ moex_status moex_paged_attention(const void* q, int64_t ldq, const moex_paged_kv
 
 /*
  * Keys and values of one layer in pages, as Q8_0 blocks: 32 int8 values and
- * one FP16 scale, value = scale * int8 (34 bytes in place of 64).  Element d of
+ * one FP16 scale of either sign, value = scale * int8 (34 bytes in place of 64).
+ * Element d of
  * key head h of the token in slot r of page p is at
  *   k + p*page_stride + h*head_stride + r*row_stride + d            (int8)
  * and the scale of its block at

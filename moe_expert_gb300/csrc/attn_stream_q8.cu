@@ -170,13 +170,14 @@ struct RowScales {
     const __half2 h = *reinterpret_cast<const __half2*>(&w[b >> 1]);
     return b & 1 ? __high2float(h) : __low2float(h);
   }
-  // A power of two above every scale, as its exponent (-14 for subnormal ones, 17 and more for those that are
-  // negative or not finite).
+  // A power of two above every scale's magnitude, as its exponent (-14 for zeros and subnormal ones, 17 for those that
+  // are not finite).
   __device__ __forceinline__ float exponent() const {
-    uint32_t m = w[0];
-    if constexpr (NB == 4) m = __vmaxu2(m, w[1]);
+    constexpr uint32_t MAGNITUDE = 0x7FFF7FFFu;
+    uint32_t m = w[0] & MAGNITUDE;
+    if constexpr (NB == 4) m = __vmaxu2(m, w[1] & MAGNITUDE);
     m = __vmaxu2(m, m >> 16);
-    return __uint_as_float(0x4B000000u | (m >> 10 & 0x3Fu)) - 8388622.f;  // 2^23 + n, less 2^23 + 14
+    return __uint_as_float(0x4B000000u | (m >> 10 & 0x1Fu)) - 8388622.f;  // 2^23 + n, less 2^23 + 14
   }
 };
 
