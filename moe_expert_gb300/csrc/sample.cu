@@ -22,8 +22,8 @@
 // Latency bounds few rows (steps of a cluster one after the other: 3 to 5 joint
 // barriers), instructions and the shared memory of a row, which lets some 50 rows of 128256
 // run at a time, many.  Measured, device time: one row of 128256, top-k 50 and top-p
-// 0.95, 8.6 us; top-p alone 18.1 us; 64 rows of 128256 by settings of their own, top-p,
-// 54 us; 200 rows of 50001 BF16, min-p, 17.0 us.
+// 0.95, 8.7 us; top-p alone 17.9 us; 64 rows of 128256 by settings of their own, top-p,
+// 53.4 us (48 rows 42.3); 200 rows of 50001 BF16, min-p, 16.9 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -67,27 +67,23 @@ __device__ __forceinline__ uint64_t rank_key(float x, int i) {
 // Powers of two that x lies below the largest logit, times 1 / T (0, and not NaN, for +inf below +inf).
 __device__ __forceinline__ float depth(float x, float top, float c) { return fmaxf((top - x) * c, 0.f); }
 
-// A mass in units of 2^-43, as hi * 2^23 + lo: an FP32 number added to 8 has its bits down to 2^-20 in the low
-// word, and what is left, added to 1.5 2^-20, those down to 2^-43.
-struct Mass {
-  uint32_t hi;
-  int32_t lo;
-  __device__ __forceinline__ uint64_t whole() const { return (static_cast<uint64_t>(hi) << 23) + static_cast<int64_t>(lo); }
-};
 __device__ __forceinline__ float exp2_below(float y) {  // 2^-y
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-y));
   return e;
 }
-struct MassSum {  // of up to 100 masses: their words' bits, the two numbers' own taken off at the end
+// A sum of up to 100 masses in units of 2^-43, as hi * 2^23 + lo: an FP32 number added to 8, rounded down, has its bits
+// down to 2^-20 in the low word, and what is left, added to 2^-20, those down to 2^-43, rounded to the nearest.  The words'
+// bits are added, and the two numbers' own taken off at the end.
+struct MassSum {
   uint32_t hi = 0, lo = 0, n = 0;
   __device__ __forceinline__ float add(float e) {  // e to the nearest unit, which is what was added
-    const float t = e + 8.f, up = t - 8.f, r = e - up + 0x1.8p-20f;
+    const float t = __fadd_rd(e, 8.f), less = t - (8.f + 0x1p-20f), r = e - less;
     hi += __float_as_uint(t), lo += __float_as_uint(r), ++n;
-    return up + (r - 0x1.8p-20f);
+    return less + r;
   }
   __device__ __forceinline__ uint64_t whole() const {
-    return Mass{hi - n * __float_as_uint(8.f), static_cast<int32_t>(lo - n * __float_as_uint(0x1.8p-20f))}.whole();
+    return (static_cast<uint64_t>(hi - n * __float_as_uint(8.f)) << 23) + (lo - n * __float_as_uint(0x1p-20f));
   }
 };
 __device__ __forceinline__ uint64_t mass_of(float e) {
@@ -103,8 +99,8 @@ __device__ __forceinline__ float in_units(float e) {
 // Sixteenths of a power of two downwards from 1, as a mass's own bits give them: bin b of e = 2^-(b / 8) (1 - r 2^-24),
 // b % 8 the upper three bits of r's 23; BINS - 1 for what lies beyond.  A bin's sum has to be that of its tokens' masses to
 // the last unit, so that a cut which the sum puts into a bin is found among the bin's tokens: e is a whole number of units
-// here (below 2^-20 FP32 holds finer ones).  64 rows of 128256 take 54.3 us with the rounding and 53.5 without; in a second
-// pass, for cuts below 2^-20 only, it costs those rows a third more and the others as much.
+// here (below 2^-20 FP32 holds finer ones), which the sum's own four additions leave: rounding by two more took 64 rows of
+// 128256 54.3 us in place of 53.4, in a second pass, for cuts below 2^-20 only, 55.2.
 __device__ __forceinline__ uint32_t below_one(float e) { return 0x3F800000u - __float_as_uint(e); }
 
 // x in [0, 1) in units of 2^-64, exactly from 2^-41 on: shares of 64-bit sums are then integer products (FP64 arithmetic
@@ -142,7 +138,8 @@ struct Shared {
   uint32_t n_list;
 };
 
-// Threads of a CTA: FEW where every CTA has an SM of its own, MANY, three CTAs an SM, otherwise.  Measured, device time,
+// Threads of a CTA: FEW where every CTA has an SM of its own, MANY, three CTAs an SM where slices are of 16384 logits at most
+// (two with rows of 151936, one with rows of 262144), otherwise.  Measured, device time,
 // one row of 128256 FP32 logits with top-k 50 and top-p 0.95 / with top-p alone: 384 threads 8.7 / 21.4 us, 512
 // 8.7 / 19.3, 768 10.1 / 20.7, 1024 10.9 / 21.2; 64 rows with top-p alone / 200 rows of 50001 with min-p: 384 threads
 // three an SM 55.1 / 17.1 us, 512 two an SM 52.6 / 21.4.
@@ -740,7 +737,8 @@ cudaError_t launch(SampleArgs a, int n_rows, int cluster, cudaStream_t s) {
 
 template <int TYPE>
 cudaError_t launch(const SampleArgs& a, int n_rows, cudaStream_t s) {
-  // CTAs of a row: slices of at most 16384 logits; with few rows, as many CTAs as a cluster has, while every CTA of every
+  // CTAs of a row: slices of at most 16384 logits, while a cluster has CTAs (up to 131072 logits; of 32768 beyond: 64 rows
+  // of 151936 67 us, of 262144 189); with few rows, as many CTAs as a cluster has, while every CTA of every
   // row has an SM of its own (FEW's registers let one run on an SM; 16 rows of 128256 in 16 clusters of 8, where 15 run at
   // a time: 13.2 us, by MANY 10.7; 37 rows of 5000 in clusters of 4, where 36 do: 7.6, of 2: 5.2).
   const auto alone = [](int cluster) {

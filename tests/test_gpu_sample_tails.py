@@ -65,3 +65,19 @@ def test_a_row_gets_the_same_in_every_batch(V, many, every):
                 i, q = m.sample_tokens(x[at:at + size], u[at:at + size], top_p=p)
                 assert torch.equal(i, ids[at:at + size]) and torch.equal(q, prob[at:at + size]), (shift, p, size, at)
     assert status() == 0
+
+
+def test_ends_of_fp32():
+    """Temperatures below 4.8e-39 count as that, a difference of logits beyond FP32's largest number as infinite."""
+    import torch
+    m = mx()
+    big = float(np.finfo(np.float32).max)
+    u = torch.tensor([0.01, LAST], device="cuda")
+    x = torch.tensor([[3.0, 3.5, -7.0], [-7.0, 3.5, 3.0]], device="cuda")
+    for t in (1e-45, 1e-40, 5e-39):
+        ids, prob = m.sample_tokens(x, u, temperature=t, top_p=0.9)
+        assert ids.tolist() == [1, 1] and prob.tolist() == [1, 1]
+    x = torch.tensor([[-big, big, -big], [-big, 0.0, big]], device="cuda")
+    ids, prob = m.sample_tokens(x, u, temperature=1e38)
+    e = float(np.exp(-big / 1e38))     # of a difference that FP32 holds
+    assert ids.tolist() == [1, 2] and prob[0] == 1 and abs(prob[1].item() * (1 + e) - 1) < 1e-5 and status() == 0
