@@ -526,8 +526,7 @@ moex_status moex_paged_attention(const void* q, int64_t ldq, const moex_paged_kv
 /*
  * Keys and values of one layer in pages, as Q8_0 blocks: 32 int8 values and
  * one FP16 scale of either sign, value = scale * int8 (34 bytes in place of 64).
- * Element d of
- * key head h of the token in slot r of page p is at
+ * Element d of key head h of the token in slot r of page p is at
  *   k + p*page_stride + h*head_stride + r*row_stride + d            (int8)
  * and the scale of its block at
  *   k_scale + p*sc_page_stride + h*sc_head_stride + r*sc_row_stride + d/32  (FP16);
@@ -597,7 +596,10 @@ size_t moex_paged_attention_q8_workspace_bytes(const moex_paged_kv_q8* kv, const
  * single tokens, drafted ones and short pieces.  (Any number of tokens is
  * taken, but every 16 rows of a key head -- tokens times its query heads -- read
  * the keys again: from about 100 rows on, prompts for instance, moex_kv_read_q8
- * and moex_paged_attention are faster.)
+ * and moex_paged_attention are faster.)  Few sequences are faster over a page
+ * table that is cut to the longest of them: up to 4096 positions (8192 with heads
+ * of 64) a tile is one cluster's and there is one launch without a workspace, with
+ * more positions in the table there are two, whatever ctx_len says.
  * Scores, their maximum and sum, and the accumulated output are FP32;
  * probability times value scale is rounded to FP16 for the second product, and
  * queries are brought into FP16's range by a power of two.
@@ -641,8 +643,11 @@ typedef struct moex_sampling {
  * NaN is masked; a row of masked logits gives id -1 and prob 0; logits of +inf
  * share everything.  u below 0 counts as 0, 1 and above as the largest number
  * below 1.  A NaN among a row's u and settings, or a negative or infinite
- * temperature, gives id -1 and prob 0, and is flagged.  Sums are exact (64-bit
- * integers), so results do not depend on the order in which blocks run.
+ * temperature, gives id -1 and prob 0, and is flagged.  e is FP32, to the nearest
+ * multiple of 2^-43, and sums of it are exact (64-bit integers), so results do not
+ * depend on the order in which blocks run, nor a row's on the other rows of the call.
+ * Differences of logits are FP32's: one beyond its largest number is infinite
+ * (e = 0).  A temperature above 0 and below 4.8e-39 counts as that.
  *   logits : device [n_rows][V] of type F32, BF16 or F16, row r at logits + r*ldl.
  *   u      : device FP32 [n_rows].
  *   ids    : device int32 [n_rows];  prob : device FP32 [n_rows] or NULL.

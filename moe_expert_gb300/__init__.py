@@ -607,7 +607,9 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, cu_q, ctx_len, pag
     as it is: for single tokens, drafted ones and short pieces.  q bfloat16 or
     float16; the rest as paged_attention.  From about 100 rows a key head on
     (tokens times its query heads: prompts), kv_read_q8 and paged_attention are
-    faster."""
+    faster.  Few sequences are faster with page_table cut to the longest context
+    (page_table[:, :pages]: rows need not be packed): one launch up to 4096
+    positions, 8192 with heads of 64."""
     return (_native_module or _load_native()).paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, cu_q, ctx_len,
                                                                  page_table, max_q, scale, window, out, out_dtype, lse,
                                                                  ws, _handle(stream))

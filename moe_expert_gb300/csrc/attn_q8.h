@@ -20,8 +20,8 @@ constexpr int q8_step(int D) { return D == 64 ? 32 : 16; }
 // over 1003 keys 7.5 us instead of 6.7.)
 constexpr int q8_ctas(int D, int NT) { return D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
 
-// The most CTAs of a cluster, and the most units of one of them: with more, ranges over all SMs and a second kernel that
-// joins them are faster.  Measured, heads of 128, 8 key heads, ranges / clusters: one token over 1000 keys 9.4 / 6.7 us,
+// The most CTAs of a cluster, and the most units of one of them, as far as the host knows (the page table's positions, not
+// the lengths on the device): with more, ranges over all SMs and a second kernel that joins them are faster.  Measured, heads of 128, 8 key heads, ranges / clusters: one token over 1000 keys 9.4 / 6.7 us,
 // 4000 keys 11.7 / 10.0, 8000 keys (16 units a CTA) 13.2 / 14.6, 16000 keys 18.3 / 24.5; 8 tokens over up to 1000 keys
 // 10.9 / 8.6, 2000 keys 11.9 / 11.4, 4000 keys (16 units a CTA) 17.3 / 17.7; 16 tokens over 1000 keys 11.9 / 11.0.
 constexpr int Q8_CLUSTER = 8, Q8_CLUSTER_STEPS = 8;

@@ -33,7 +33,8 @@
 //
 // Measured, device time: 64 single tokens over contexts to 16384, 4 query heads a key
 // head, 98 us, 90% of the copy rate (copies alone 93 us); three over up to 100001 keys
-// 41 us (copies alone 33); one token over 1003 keys 6.6 us.
+// 41 us (copies alone 33); one token over 1003 keys, its page table cut to 63 pages of 16,
+// 6.6 us (2048 pages 9.2 us: ranges and the joining kernel).
 #include <cooperative_groups.h>
 
 #include <cfloat>

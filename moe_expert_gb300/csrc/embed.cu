@@ -9,10 +9,11 @@ namespace moex {
 // and the rounding to the output's type.  A thread takes a word of quants at a
 // time: four values of Q8_0, or the eight of IQ4_NL whose nibbles share four
 // bytes (values j and j + 16 of a block), so neighbouring lanes read and write
-// whole lines; blockDim.y rows a CTA.  DRAM bounds it for many tokens (8192 rows
-// of 2560, IQ4_NL to FP32: 19.3 us, 74% of the copy rate; one value's conversion by
-// an integer-to-float instruction and a 64-bit division a thread 30.3 us), the two
-// dependent reads (id, row) for few.
+// whole lines; blockDim.y rows a CTA.  For many tokens the two dependent reads
+// (id, row) and the instructions bound it (59% of the issue slots; 8192 rows of 2560,
+// IQ4_NL to FP32: 19.3 to 19.7 us, 73% of the copy rate, where a kernel that only writes
+// as many bytes takes 12.2; one value's conversion by an integer-to-float instruction and a
+// 64-bit division a thread 30.3 us), for few the reads alone.
 template <int FMT, int YT>
 __global__ void __launch_bounds__(256) embed_kernel(const uint8_t* __restrict__ qs, const uint8_t* __restrict__ scales,
                                                     int64_t rows, int words, int64_t sc_row,

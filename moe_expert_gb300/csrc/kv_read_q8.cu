@@ -23,7 +23,8 @@ constexpr int READ_THREADS = 128, READ_HEADS = 2;
 // are looked up once, and the heads' reads (8 bytes and a scale, keys and values) are
 // independent.  Neighbouring threads take neighbouring features, so stores are whole
 // lines of 16 bytes a thread.  DRAM bounds it for many positions (4926 of 8 heads of
-// 128 / 16384 of 8 heads of 64: 8.7 / 11.4 us, 87 / 67% of the copy rate), the three reads
+// 128 / 16384 of 8 heads of 64: 8.7 / 11.4 us, 87 / 67% of the copy rate; with heads of 64 the
+// instructions too, 64% of the issue slots), the three reads
 // one after the other (lengths, page, values) for few.  A position's page is asked for
 // with the values of the one before (without, 256 threads: 9.4 / 12.1 us; with one head a
 // thread 10.3 / 13.0, with four, not ahead, 10.0 / 12.4).
